@@ -31,5 +31,12 @@ from ._lib import (  # noqa: F401
     moe_status_string,
     moe_workspace_bytes,
 )
+from .operators import (  # noqa: F401
+    moe_block_norm,
+    moe_combine,
+    moe_grouped_gemm,
+    moe_int8_gemm,
+    moe_int8_quantize,
+)
 
 load()

@@ -23,7 +23,7 @@ EXPORTS = (
     "moe_status_string", "moe_last_cuda_error", "moe_route", "moe_permute", "moe_gate_up_swiglu",
     "moe_down_combine", "moe_mxfp4_forward", "moe_workspace_bytes", "moe_forward_launches", "moe_mxfp4_forward_ex",
     "moe_mxfp4_forward_profile", "moe_route_noalloc", "moe_selftest_wait_timeout", "moe_mxfp4_forward_partial",
-    "moe_reduce_partials",
+    "moe_reduce_partials", "moe_block_norm", "moe_int8_quantize", "moe_int8_gemm", "moe_grouped_gemm", "moe_combine",
 )
 PROFILE_KERNELS = ("route_logits", "route_select", "permute", "gate_up", "gather", "gate_up_tc_small",
                    "gate_up_tc_large", "down", "down_tc_small", "down_tc_large", "combine")
@@ -80,6 +80,17 @@ def load():
     lib.moe_mxfp4_forward_partial.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, P, P, P, P, S, P]
     lib.moe_reduce_partials.restype = I
     lib.moe_reduce_partials.argtypes = [P, I, P, I, I, P]
+    F = ctypes.c_float
+    lib.moe_block_norm.restype = I
+    lib.moe_block_norm.argtypes = [P, P, P, P, I, P, F, F, F, F, P, P, P, P, I, I, P]
+    lib.moe_int8_quantize.restype = I
+    lib.moe_int8_quantize.argtypes = [P, I, P, P, I, I, P]
+    lib.moe_int8_gemm.restype = I
+    lib.moe_int8_gemm.argtypes = [P, P, P, P, P, P, I, I, I, I, P, P]
+    lib.moe_grouped_gemm.restype = I
+    lib.moe_grouped_gemm.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, P, P]
+    lib.moe_combine.restype = I
+    lib.moe_combine.argtypes = [P, I, P, P, P, P, I, I, I, P]
     _lib = lib
     return lib
 

@@ -12,6 +12,7 @@
 #include "down_slab.h"
 #include "moe.h"
 #include "moe_internal.h"
+#include "ops.h"
 
 namespace moe {
 
@@ -195,6 +196,27 @@ static int make_act_map(CUtensorMap *map, const void *base, uint64_t rows, uint6
     CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue);
+    return MOE_OK;
+}
+
+// Map of up to 5 dimensions with 128-byte-swizzled boxes (128 bytes of the innermost dimension each);
+// reads outside the tensor fill with zeros.  strides[i] is the byte stride of dimension i + 1.
+int encode_sw128_map(CUtensorMap *map, CUtensorMapDataType type, uint32_t rank, const void *base, const uint64_t *dims,
+                     const uint64_t *strides, const uint32_t *box)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return cuda_fail(cudaErrorNotSupported);
+    cuuint64_t d[5], st[4];
+    cuuint32_t b[5];
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    for (uint32_t i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        if (i + 1 < rank) st[i] = strides[i];
+    }
+    CUresult r = fn(map, type, rank, const_cast<void *>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue);
     return MOE_OK;
 }

@@ -1,0 +1,62 @@
+// ops.h -- declarations of the operators around the routed layer: block norms and int8 codes
+// (block_norm.cu), ragged products (ragged_gemm.cu), the weighted combine of expert rows
+// (combine.cu).  Their C entry points are in ops_api.cu.  Not part of the public ABI.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "moe_internal.h"
+
+namespace moe {
+
+constexpr int kMaxRowElems = 16384;      // longest row of block_norm and of the quantiser
+constexpr int kMaxProductDim = 65536;    // N and K of the products
+constexpr int kMaxProductRows = 1 << 22;
+
+struct NormArgs {
+    const __nv_bfloat16 *x, *residual, *w_post, *w_pre;
+    const void *gate;
+    __nv_bfloat16 *res_out, *h_out;
+    int8_t *q_out;
+    float *q_s;
+    float block_scale, residual_scale, eps, w_offset;
+    int gate_kind;
+    int M, H;
+};
+cudaError_t launch_block_norm(const NormArgs &a, cudaStream_t s);
+cudaError_t launch_int8_quantize(const __nv_bfloat16 *x, bool swiglu, int8_t *q, float *q_s, int M, int K,
+                                 cudaStream_t s);
+cudaError_t launch_combine_rows(const void *y, bool y_f32, const float *topk_w, const int32_t *inv_pos,
+                                const __nv_bfloat16 *add, __nv_bfloat16 *out, int M, int H, int k, cudaStream_t s);
+
+// How a ragged product is cut: tiles of 128 weight rows x up to nt tokens, K over `split` CTAs.
+struct RaggedPlan {
+    int nt, stages, smem;
+    int row_blocks, kblocks;
+    int max_tiles;   // upper bound of the token tiles of any offsets
+    int split;
+};
+RaggedPlan ragged_plan(int R, int N, int K, int E, bool int8, bool swiglu);
+
+struct RaggedArgs {
+    const int32_t *offsets;      // [E+1]; nullptr: one group of all R rows
+    const int32_t *sorted_ids;   // nullptr: the rows of x are the rows of y
+    const float *row_scale, *col_scale;   // int8
+    const __nv_bfloat16 *add;             // int8, nullable
+    void *y;
+    int32_t *status_out;
+    int y_f32;
+    int R, M, N, E, k;
+    int nt, stages, row_blocks, kblocks, split;
+};
+cudaError_t launch_ragged(bool int8, bool swiglu, const CUtensorMap &wmap, const CUtensorMap &xmap, const RaggedArgs &a,
+                          const RaggedPlan &p, cudaStream_t s);
+
+// cuTensorMapEncodeTiled for a tiled map of 128-byte-swizzled boxes; MOE_OK or MOE_ERR_CUDA (api.cu).
+int encode_sw128_map(CUtensorMap *map, CUtensorMapDataType type, uint32_t rank, const void *base, const uint64_t *dims,
+                     const uint64_t *strides, const uint32_t *box);
+
+}  // namespace moe

@@ -270,6 +270,85 @@ int moe_mxfp4_forward_profile(const void *x, const float *router_w, const float 
                               void *workspace, size_t workspace_bytes, cudaStream_t stream,
                               float *kernel_ms);
 
+/*
+ * Operators around the routed layer: the norms and the residual of the decoder block that holds it, its
+ * shared (dense) expert in 8-bit integers, and experts whose weights are bf16.  The pages have no
+ * counterpart; these are interface choices of this library.  Conventions as above, and:
+ *   - none of them uses a workspace, so calls on different streams and captured graphs share nothing;
+ *   - activations bf16, sums in fp32 (int32 for int8 products), one rounding per output;
+ *   - NaN and Inf in a row stay in that row's outputs (int8 codes of such a row are undefined);
+ *   - outputs may not overlap inputs except where a function says so.
+ */
+
+/* Gate of moe_block_norm. */
+#define MOE_GATE_NONE 0
+#define MOE_GATE_CHANNEL 1   /* bf16 [H], the same for every token */
+#define MOE_GATE_TOKEN 2     /* fp32 [M], one factor per token */
+#define MOE_GATE_FULL 3      /* bf16 [M,H] */
+
+/*
+ * The norms before and after a block, with the block's gate and the residual scale, in one pass:
+ *   z  = x * rsqrt(mean(x^2) + eps) * (w_post + w_offset)      (w_post NULL: z = x)
+ *   r' = block_scale * gate * z + residual_scale * residual    (residual NULL: without it)
+ *   h  = r' * rsqrt(mean(r'^2) + eps) * (w_pre + w_offset)
+ * x, residual bf16 [M,H]; w_post, w_pre bf16 [H] (w_offset 1 for checkpoints that store weight - 1);
+ * means over the H elements of a token.  Outputs, any of which may be NULL but not all: res_out
+ * bf16 [M,H] = r'; h_out bf16 [M,H] = h; q_out int8 [M,H] with q_s fp32 [M] = the codes of h as
+ * moe_int8_quantize makes them.  h is computed from r' before its rounding.  w_pre is given exactly
+ * when h_out or q_out is.  With neither w_post, gate nor residual it is the plain norm before a block.
+ * res_out or h_out may be x or residual itself (the same pointer).  H a multiple of 8, at most 16384;
+ * eps > 0.  Out of contract: rows whose sum of squares overflows fp32.
+ */
+int moe_block_norm(const void *x_bf16, const void *residual_bf16, const void *w_post_bf16, const void *gate,
+                   int gate_kind, const void *w_pre_bf16, float block_scale, float residual_scale, float eps,
+                   float w_offset, void *res_out_bf16, void *h_out_bf16, int8_t *q_out, float *q_s, int M, int H,
+                   cudaStream_t stream);
+
+/*
+ * Symmetric 8-bit codes of rows, the activations of moe_int8_gemm:
+ *   q_s[m] = max_c |v[m,c]| / 127,  q[m,c] = round-half-even(v[m,c] / q_s[m])   (a row of zeros: 0, codes 0)
+ * with v = x (bf16 [M,K]) or, swiglu != 0, v = silu(min(g,7)) * clamp(u,-7,7) of x = [g | u] (bf16 [M,2K]:
+ * K gate columns, then K up columns), kept in fp32.  K a multiple of 16, at most 16384.
+ */
+int moe_int8_quantize(const void *x_bf16, int swiglu, int8_t *q, float *q_s, int M, int K, cudaStream_t stream);
+
+/*
+ * Product in 8-bit integers with a scale for each token and each output channel:
+ *   out[m,n] = q_s[m] * w_s[n] * sum_c q[m,c] * w_q[n,c]  (+ add[m,n])
+ * q int8 [M,K], q_s fp32 [M]; w_q int8 [N,K], w_s fp32 [N]; add bf16 [M,N] (nullable); out bf16 [M,N],
+ * or fp32 when out_f32.  The sum is exact (int32).  A bf16 out may be add itself.  Any M and N up to
+ * 4194304 and 65536; K a multiple of 16, at most 65536.  status_out (nullable, device int32) receives
+ * MOE_OK or MOE_ERR_TIMEOUT once the enqueued work has run.
+ */
+int moe_int8_gemm(const int8_t *q, const float *q_s, const int8_t *w_q, const float *w_s, const void *add_bf16,
+                  void *out, int out_f32, int M, int N, int K, int32_t *status_out, cudaStream_t stream);
+
+/*
+ * Products grouped by expert with groups of any size: for every position p of the expert-grouped order
+ * and the expert e whose range expert_offsets[e] .. expert_offsets[e+1]-1 holds p
+ *   y[p] = w[e] x[row(p)]                                   (w bf16 [E,N,K])
+ *   y[p] = silu(min(g,7)) * clamp(u,-7,7), [g;u] = w[e] x[row(p)]   (swiglu: w bf16 [E,2N,K], gate rows
+ *                                                            0..N-1 then up rows; N a multiple of 16)
+ * row(p) = sorted_ids[p] / k with x bf16 [M,K] (the routed gather), or p with x bf16 [M*k,K] when
+ * sorted_ids is NULL.  expert_offsets int32 [E+1] and sorted_ids int32 [M*k] as moe_permute writes them;
+ * offsets ascend within 0..M*k.  Positions outside every range are left as they were in y.
+ * y bf16 [M*k,N], or fp32 when y_f32.  bf16 products, fp32 sums.  K a multiple of 8 up to 65536, N up to
+ * 65536, E <= 1024, k <= 32, M*k <= 4194304.  status_out as in moe_int8_gemm.
+ */
+int moe_grouped_gemm(const void *x_bf16, const void *w_bf16, const int32_t *expert_offsets, const int32_t *sorted_ids,
+                     void *y, int y_f32, int swiglu, int M, int N, int K, int E, int k, int32_t *status_out,
+                     cudaStream_t stream);
+
+/*
+ * Weighted sum of each token's k rows of an expert-grouped y (bf16 [M*k,H], or fp32 when y_f32):
+ *   out[t] = bf16( sum_j topk_w[t,j] * y[inv_pos[t*k+j]] (+ add[t]) ),   in slot order, fp32
+ * inv_pos int32 [M*k] as moe_permute writes it; a position outside 0..M*k-1 marks a dropped assignment
+ * and contributes nothing.  add bf16 [M,H] (nullable) may be out itself.  H a multiple of 8 up to 65536,
+ * k <= 32, M*k <= 4194304.
+ */
+int moe_combine(const void *y, int y_f32, const float *topk_w, const int32_t *inv_pos, const void *add_bf16,
+                void *out_bf16, int M, int H, int k, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
