@@ -200,22 +200,17 @@ static int make_act_map(CUtensorMap *map, const void *base, uint64_t rows, uint6
     return MOE_OK;
 }
 
-// Map of up to 5 dimensions with 128-byte-swizzled boxes (128 bytes of the innermost dimension each);
-// reads outside the tensor fill with zeros.  strides[i] is the byte stride of dimension i + 1.
-int encode_sw128_map(CUtensorMap *map, CUtensorMapDataType type, uint32_t rank, const void *base, const uint64_t *dims,
-                     const uint64_t *strides, const uint32_t *box)
+// Row-major [rows][K] matrix of bytes or bf16 for the operators around the layer: boxes of 128 bytes x box_rows.
+int encode_rows_map(CUtensorMap *map, bool bytes, const void *base, uint64_t rows, uint64_t K, uint32_t box_rows)
 {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return cuda_fail(cudaErrorNotSupported);
-    cuuint64_t d[5], st[4];
-    cuuint32_t b[5];
-    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-    for (uint32_t i = 0; i < rank; ++i) {
-        d[i] = dims[i];
-        b[i] = box[i];
-        if (i + 1 < rank) st[i] = strides[i];
-    }
-    CUresult r = fn(map, type, rank, const_cast<void *>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    const cuuint64_t dims[2] = {K, rows};
+    const cuuint64_t strides[1] = {K * (bytes ? 1 : 2)};
+    const cuuint32_t box[2] = {bytes ? 128u : 64u, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    CUresult r = fn(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                    const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue);
     return MOE_OK;

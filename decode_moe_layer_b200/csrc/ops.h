@@ -32,31 +32,43 @@ cudaError_t launch_int8_quantize(const __nv_bfloat16 *x, bool swiglu, int8_t *q,
 cudaError_t launch_combine_rows(const void *y, bool y_f32, const float *topk_w, const int32_t *inv_pos,
                                 const __nv_bfloat16 *add, __nv_bfloat16 *out, int M, int H, int k, cudaStream_t s);
 
-// How a ragged product is cut: tiles of 128 weight rows x up to nt tokens, K over `split` CTAs.
+// How a ragged product is cut: tiles of 128 weight rows x up to nt tokens with K over `split` CTAs
+// (ragged_gemm.cu), or tiles of 256 x 256 on CTA pairs (wide, ragged_wide.cu).
 struct RaggedPlan {
+    bool wide;
     int nt, stages, smem;
-    int row_blocks, kblocks;
-    int max_tiles;   // upper bound of the token tiles of any offsets
+    int box_rows;              // token rows per TMA box (!wide)
+    int row_blocks, kblocks;   // of 128 weight rows (swiglu: 64 output columns), of 128 bytes of K
+    int max_tiles;             // !wide: upper bound of the token tiles of any offsets
     int split;
+    int threads;               // wide
 };
-RaggedPlan ragged_plan(int R, int N, int K, int E, bool int8, bool swiglu);
+RaggedPlan ragged_plan(int R, int N, int K, int E, bool int8, bool swiglu, bool gather);
+void wide_plan(RaggedPlan &p, int E, bool gather);
 
 struct RaggedArgs {
     const int32_t *offsets;      // [E+1]; nullptr: one group of all R rows
     const int32_t *sorted_ids;   // nullptr: the rows of x are the rows of y
+    const void *x;
     const float *row_scale, *col_scale;   // int8
     const __nv_bfloat16 *add;             // int8, nullable
     void *y;
     int32_t *status_out;
     int y_f32;
-    int R, M, N, E, k;
-    int nt, stages, row_blocks, kblocks, split;
+    int R, M, N, K, E, k;
+    int nt, stages, row_blocks, kblocks, split, box_rows;
+};
+// Maps of the same rows with boxes of 16, 32, 64 and 128 of them.
+struct BoxMaps {
+    CUtensorMap m[4];
 };
 cudaError_t launch_ragged(bool int8, bool swiglu, const CUtensorMap &wmap, const CUtensorMap &xmap, const RaggedArgs &a,
                           const RaggedPlan &p, cudaStream_t s);
+cudaError_t launch_ragged_wide(bool int8, bool swiglu, const CUtensorMap &wmap, const BoxMaps &xmaps,
+                               const RaggedArgs &a, const RaggedPlan &p, cudaStream_t s);
 
-// cuTensorMapEncodeTiled for a tiled map of 128-byte-swizzled boxes; MOE_OK or MOE_ERR_CUDA (api.cu).
-int encode_sw128_map(CUtensorMap *map, CUtensorMapDataType type, uint32_t rank, const void *base, const uint64_t *dims,
-                     const uint64_t *strides, const uint32_t *box);
+// Map of a row-major [rows][K] matrix of 8-bit or bf16 elements: boxes of 128 bytes x box_rows, 128-byte
+// swizzle, zeros outside; MOE_OK or MOE_ERR_CUDA (api.cu).
+int encode_rows_map(CUtensorMap *map, bool bytes, const void *base, uint64_t rows, uint64_t K, uint32_t box_rows);
 
 }  // namespace moe

@@ -28,6 +28,44 @@ static bool bad_overlap(const void *out, size_t on, const void *in, size_t n, bo
 
 static bool finite_f(float v) { return v - v == 0.0f; }
 
+// Maps and launch of a ragged product whose arguments have been checked: w [w_rows][K], x [a.M][K].
+static int run_ragged(bool int8, bool swiglu, const void *w, uint64_t w_rows, RaggedArgs &a, cudaStream_t stream)
+{
+    const bool gather = a.sorted_ids != nullptr;
+    const RaggedPlan p = ragged_plan(a.R, a.N, a.K, a.E, int8, swiglu, gather);
+    a.nt = p.nt;
+    a.stages = p.stages;
+    a.box_rows = p.box_rows;
+    a.row_blocks = p.row_blocks;
+    a.kblocks = p.kblocks;
+    a.split = p.split;
+    // weight boxes of 128 rows, or (swiglu) of 64 gate rows and of 64 up rows
+    CUtensorMap wmap;
+    int rc = encode_rows_map(&wmap, int8, w, w_rows, static_cast<uint64_t>(a.K), swiglu ? 64 : 128);
+    if (rc != MOE_OK) return rc;
+    const uint64_t rows = static_cast<uint64_t>(a.M), K = static_cast<uint64_t>(a.K);
+    if (p.wide) {
+        BoxMaps maps = {};
+        for (int i = 0; i < 4 && !gather; ++i) {
+            rc = encode_rows_map(&maps.m[i], int8, a.x, rows, K, 16u << i);
+            if (rc != MOE_OK) return rc;
+        }
+        if (a.status_out) {
+            const cudaError_t e = cudaMemsetAsync(a.status_out, 0, sizeof(int32_t), stream);
+            if (e != cudaSuccess) return cuda_fail(e);
+        }
+        const cudaError_t e = launch_ragged_wide(int8, swiglu, wmap, maps, a, p, stream);
+        return e == cudaSuccess ? MOE_OK : cuda_fail(e);
+    }
+    CUtensorMap xmap;   // one row high for the gather
+    rc = encode_rows_map(&xmap, int8, a.x, rows, K, gather ? 1u : static_cast<uint32_t>(p.box_rows));
+    if (rc != MOE_OK) return rc;
+    cudaError_t e = cudaSuccess;
+    if (a.status_out) e = cudaMemsetAsync(a.status_out, 0, sizeof(int32_t), stream);
+    if (e == cudaSuccess) e = launch_ragged(int8, swiglu, wmap, xmap, a, p, stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e);
+}
+
 }  // namespace moe
 
 using namespace moe;
@@ -125,18 +163,9 @@ int moe_int8_gemm(const int8_t *q, const float *q_s, const int8_t *w_q, const fl
         ranges_meet(out, on, q_s, static_cast<size_t>(M) * 4) || ranges_meet(out, on, w_s, static_cast<size_t>(N) * 4) ||
         bad_overlap(out, on, add_bf16, mn * 2, out_f32 == 0))
         return MOE_ERR_INVALID_ARG;
-    const RaggedPlan p = ragged_plan(M, N, K, 1, true, false);
-    CUtensorMap wmap, xmap;
-    const uint64_t uK = static_cast<uint64_t>(K), uN = static_cast<uint64_t>(N);
-    const uint64_t wdims[5] = {uK, uN, 1, 1, 1}, wstr[4] = {uK, uK * uN, uK * uN, uK * uN};
-    const uint32_t wbox[5] = {128, 128, 1, 1, 1};
-    int rc = encode_sw128_map(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, w_q, wdims, wstr, wbox);
-    if (rc != MOE_OK) return rc;
-    const uint64_t xdims[2] = {uK, static_cast<uint64_t>(M)}, xstr[1] = {uK};
-    const uint32_t xbox[2] = {128, 16};
-    rc = encode_sw128_map(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, q, xdims, xstr, xbox);
-    if (rc != MOE_OK) return rc;
     RaggedArgs a = {};
+    a.x = q;
+    a.K = K;
     a.row_scale = q_s;
     a.col_scale = w_s;
     a.add = static_cast<const __nv_bfloat16 *>(add_bf16);
@@ -148,14 +177,7 @@ int moe_int8_gemm(const int8_t *q, const float *q_s, const int8_t *w_q, const fl
     a.N = N;
     a.E = 1;
     a.k = 1;
-    a.nt = p.nt;
-    a.stages = p.stages;
-    a.row_blocks = p.row_blocks;
-    a.kblocks = p.kblocks;
-    a.split = p.split;
-    if (status_out) OPS_TRY(cudaMemsetAsync(status_out, 0, sizeof(int32_t), stream));
-    OPS_TRY(launch_ragged(true, false, wmap, xmap, a, p, stream));
-    return MOE_OK;
+    return run_ragged(true, false, w_q, static_cast<uint64_t>(N), a, stream);
 }
 
 int moe_grouped_gemm(const void *x_bf16, const void *w_bf16, const int32_t *expert_offsets, const int32_t *sorted_ids,
@@ -164,7 +186,7 @@ int moe_grouped_gemm(const void *x_bf16, const void *w_bf16, const int32_t *expe
 {
     if (M < 0 || N <= 0 || K <= 0 || E <= 0 || k <= 0) return MOE_ERR_INVALID_ARG;
     if (K % 8 != 0 || K > kMaxProductDim || N > kMaxProductDim || E > kMaxE || k > kMaxK ||
-        static_cast<long long>(M) * k > kMaxProductRows || (swiglu && N % 16 != 0))
+        static_cast<long long>(M) * k > kMaxProductRows)
         return MOE_ERR_UNSUPPORTED_SHAPE;
     if (M == 0) return MOE_OK;
     if (!x_bf16 || !w_bf16 || !expert_offsets || !y) return MOE_ERR_INVALID_ARG;
@@ -179,30 +201,11 @@ int moe_grouped_gemm(const void *x_bf16, const void *w_bf16, const int32_t *expe
     if (ranges_meet(y, yn, x_bf16, static_cast<size_t>(x_rows) * K * 2) || ranges_meet(y, yn, w_bf16, wn) ||
         ranges_meet(y, yn, expert_offsets, (uE + 1) * 4) || ranges_meet(y, yn, sorted_ids, static_cast<size_t>(R) * 4))
         return MOE_ERR_INVALID_ARG;
-    const RaggedPlan p = ragged_plan(R, N, K, E, false, swiglu != 0);
-    // weight boxes of 64 K x 128 rows: rows n0.. of an expert, or (swiglu; w is [E, 2N, K], gate rows then
-    // up rows) four runs of 16 gate rows and their 16 up rows, so that a TMEM warp holds both of a pair
-    CUtensorMap wmap, xmap;
-    int rc;
-    if (swiglu) {
-        const uint64_t dims[5] = {uK, 16, 2, uN / 16, uE};
-        const uint64_t str[4] = {uK * 2, uN * uK * 2, 16 * uK * 2, 2 * uN * uK * 2};
-        const uint32_t box[5] = {64, 16, 2, 4, 1};
-        rc = encode_sw128_map(&wmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, w_bf16, dims, str, box);
-    } else {
-        const uint64_t dims[5] = {uK, uN, 1, 1, uE};
-        const uint64_t str[4] = {uK * 2, uN * uK * 2, uN * uK * 2, uN * uK * 2};
-        const uint32_t box[5] = {64, 128, 1, 1, 1};
-        rc = encode_sw128_map(&wmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, w_bf16, dims, str, box);
-    }
-    if (rc != MOE_OK) return rc;
-    const uint64_t xdims[2] = {uK, static_cast<uint64_t>(x_rows)}, xstr[1] = {uK * 2};
-    const uint32_t xbox[2] = {64, sorted_ids ? 1u : 16u};   // one row high for the gather
-    rc = encode_sw128_map(&xmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x_bf16, xdims, xstr, xbox);
-    if (rc != MOE_OK) return rc;
     RaggedArgs a = {};
     a.offsets = expert_offsets;
     a.sorted_ids = sorted_ids;
+    a.x = x_bf16;
+    a.K = K;
     a.y = y;
     a.y_f32 = y_f32 != 0;
     a.status_out = status_out;
@@ -211,14 +214,7 @@ int moe_grouped_gemm(const void *x_bf16, const void *w_bf16, const int32_t *expe
     a.N = N;
     a.E = E;
     a.k = k;
-    a.nt = p.nt;
-    a.stages = p.stages;
-    a.row_blocks = p.row_blocks;
-    a.kblocks = p.kblocks;
-    a.split = p.split;
-    if (status_out) OPS_TRY(cudaMemsetAsync(status_out, 0, sizeof(int32_t), stream));
-    OPS_TRY(launch_ragged(false, swiglu != 0, wmap, xmap, a, p, stream));
-    return MOE_OK;
+    return run_ragged(false, swiglu != 0, w_bf16, uE * uN * (swiglu ? 2 : 1), a, stream);
 }
 
 int moe_combine(const void *y, int y_f32, const float *topk_w, const int32_t *inv_pos, const void *add_bf16,

@@ -1,0 +1,216 @@
+// ragged.cuh -- device helpers that the two kernels of the ragged products share (ragged_gemm.cu,
+// ragged_wide.cu): tcgen05 and TMA forms, the table of token tiles, the epilogue.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "ops.h"
+#include "tcgen05.cuh"
+
+namespace moe {
+
+namespace ragged {
+constexpr int kRows = 128;          // weight rows per CTA and tile: the lanes of tensor memory
+constexpr int kStageKBytes = 128;   // bytes of K per stage: one 128-byte swizzle row
+constexpr int kABytes = kRows * kStageKBytes;
+}  // namespace ragged
+
+// ------------------------------------------------------------------ tcgen05, both operands in shared memory
+
+// Instruction descriptor of kind::i8: s32 accumulator (bits 4-5 = 2), signed A and B (bits 7-9 and
+// 10-12 = 1), both K-major, N >> 3 in bits 17-22, M >> 4 in bits 24-28.
+__device__ __forceinline__ uint32_t umma_idesc_i8(int m, int n)
+{
+    return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// D (+)= A * B^T over 32 bytes of K: kind::f16 (16 bf16 elements) or kind::i8 (32 int8 elements), one CTA or
+// the CTA pair (issued by the pair's even CTA; each CTA holds half of A's rows and half of B's).
+template <bool kInt8, int kCtas>
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate)
+{
+#define MOE_UMMA_SS(group, kind)                                                                  \
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"                                \
+                 "tcgen05.mma.cta_group::" group ".kind::" kind " [%0], %1, %2, %3, p;\n\t}" ::"r"( \
+                     d_tmem),                                                                     \
+                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)                            \
+                 : "memory")
+    if (kCtas == 1) {
+        if (kInt8)
+            MOE_UMMA_SS("1", "i8");
+        else
+            MOE_UMMA_SS("1", "f16");
+    } else {
+        if (kInt8)
+            MOE_UMMA_SS("2", "i8");
+        else
+            MOE_UMMA_SS("2", "f16");
+    }
+#undef MOE_UMMA_SS
+}
+
+// 16 consecutive columns of this thread's TMEM lane, without waiting for them (tmem_wait_ld).
+__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&v)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+                   "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]),
+                   "=r"(v[15])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// ------------------------------------------------------------------ clusters
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The shared-memory address of CTA `rank` of the cluster that corresponds to this CTA's smem_addr.
+__device__ __forceinline__ uint32_t map_cluster(uint32_t smem_addr, uint32_t rank)
+{
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr), "r"(rank));
+    return remote;
+}
+__device__ __forceinline__ void st_cluster(uint32_t cluster_addr, uint32_t v)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+
+// ------------------------------------------------------------------ token tiles
+
+// The groups of the rows, in shared memory: lo[e] is where group e starts (lo[E] where the last ends) and
+// first[e] the number of token tiles before it.  A group of c rows is cut into ceil(c / nt) tiles of equal
+// size rounded up to 16 rows, so that no tile is left with a few rows and a full price.
+// Whole CTA; `lo` and `first` hold E + 1 ints each.  Offsets are clamped to [0, R] and to ascending order, so
+// wrong ones cannot lead out of the tensors.  Returns after a barrier.
+__device__ __forceinline__ int tile_rows(int c, int nt)
+{
+    const int t = (c + nt - 1) / nt;
+    return t <= 1 ? nt : ((c + t - 1) / t + 15) & ~15;
+}
+__device__ __forceinline__ int tile_count(int c, int nt)
+{
+    const int rows = tile_rows(c, nt);
+    return (c + rows - 1) / rows;
+}
+__device__ __forceinline__ void build_groups(const int32_t *off, int R, int E, int nt, int *lo, int *first)
+{
+    if (off != nullptr) {
+        for (int e = threadIdx.x; e <= E; e += blockDim.x) lo[e] = min(max(__ldcg(off + e), 0), R);
+    } else if (threadIdx.x == 0) {
+        lo[0] = 0;
+        lo[1] = R;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        // lanes take `per` consecutive entries of lo: running maximum, then the tiles of their groups
+        const int lane = threadIdx.x, per = (E + 32) >> 5, e0 = lane * per, e1 = min(E + 1, e0 + per);
+        int m = 0;
+        for (int e = e0; e < e1; ++e) m = max(m, lo[e]);
+        int before = m;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, before, d);
+            if (lane >= d) before = max(before, v);
+        }
+        before = __shfl_up_sync(0xffffffffu, before, 1);
+        if (lane == 0) before = 0;
+        for (int e = e0; e < e1; ++e) lo[e] = before = max(before, lo[e]);
+        __syncwarp();
+        int mine = 0;
+        for (int e = e0; e < e1 && e < E; ++e) mine += tile_count(lo[e + 1] - lo[e], nt);
+        int incl = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += v;
+        }
+        int at = incl - mine;
+        for (int e = e0; e < e1; ++e) {
+            first[e] = at;
+            if (e < E) at += tile_count(lo[e + 1] - lo[e], nt);
+        }
+    }
+    __syncthreads();
+}
+
+// ------------------------------------------------------------------ epilogue
+
+// clamp-SwiGLU that lets a NaN through (a comparison with NaN is false).
+__device__ __forceinline__ float ragged_swiglu(float g, float u)
+{
+    const float a = g > 7.0f ? 7.0f : g;
+    const float c = u > 7.0f ? 7.0f : (u < -7.0f ? -7.0f : u);
+    return a / (1.0f + expf(-a)) * c;
+}
+
+// One pair of gate and up, finished and stored at y[row][n].
+__device__ __forceinline__ void store_pair(const RaggedArgs &a, float g, float u, size_t row, int n)
+{
+    const size_t at = row * static_cast<size_t>(a.N) + n;
+    const float h = ragged_swiglu(g, u);
+    if (a.y_f32)
+        static_cast<float *>(a.y)[at] = h;
+    else
+        static_cast<__nv_bfloat16 *>(a.y)[at] = __float2bfloat16_rn(h);
+}
+
+// Finishes kCols accumulator columns (consecutive rows of y from `row`, of which `live` are the tile's) of
+// the weight row n: scales and adds (int8: rs[] the rows' scales, cs the channel's), rounds once and stores.
+// For a column a warp writes 64 consecutive bytes (bf16), whole sectors.  The common case, all columns live,
+// has no branch between columns: a thread's chain of address, conversion and store took about 120 cycles a
+// column when each column branched, and a fifth of that without.
+template <bool kInt8, int kCols>
+__device__ __forceinline__ void finish_columns(const RaggedArgs &a, const uint32_t (&v)[kCols], const float *rs, float cs,
+                                               size_t row, int live, int n)
+{
+    if (n >= a.N) return;
+    const size_t ld = static_cast<size_t>(a.N);
+    const size_t at = row * ld + n;
+    float f[kCols];
+#pragma unroll
+    for (int j = 0; j < kCols; ++j)
+        f[j] = kInt8 ? static_cast<float>(static_cast<int32_t>(v[j])) * rs[j] * cs : __uint_as_float(v[j]);
+    if (kInt8 && a.add != nullptr) {
+        const __nv_bfloat16 *add = a.add + at;
+        __nv_bfloat16 t[kCols];
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) t[j] = j < live ? add[j * ld] : __float2bfloat16_rn(0.f);
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) f[j] += __bfloat162float(t[j]);
+    }
+    if (a.y_f32) {
+        float *y = static_cast<float *>(a.y) + at;
+        if (live >= kCols) {
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) y[j * ld] = f[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < kCols; ++j)
+                if (j < live) y[j * ld] = f[j];
+        }
+    } else {
+        __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(a.y) + at;
+        if (live >= kCols) {
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) y[j * ld] = __float2bfloat16_rn(f[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kCols; ++j)
+                if (j < live) y[j * ld] = __float2bfloat16_rn(f[j]);
+        }
+    }
+}
+
+}  // namespace moe

@@ -11,71 +11,31 @@
 // the group: a tile of `count` tokens runs MMAs of N = count rounded up to 16, so a group of one row
 // costs what one row costs, and rows beyond a group reach only accumulator columns that nobody stores.
 //
-// ragged_gemm_kernel: one tile (128 weight rows x up to `nt` tokens) per cluster of `split` CTAs.  The
-// CTAs of a cluster take consecutive ranges of K; each holds a partial accumulator, sends the columns
-// that another CTA owns into that CTA's shared memory and sums its own in rank order, so the result
-// does not depend on timing and no workspace is needed.  Warp 0 issues the TMA copies (weights as one
-// box, tokens as 16-row boxes or, by the routing's indices, four rows at a time), warp 1 the MMAs; all
-// four warps store.  The tile of a cluster is found from the group offsets on the device.
+// This file has the kernel for few rows per group and the choice between it and the one for many
+// (ragged_wide.cu).  ragged_gemm_kernel: one tile (128 weight rows x up to `nt` tokens) per cluster of
+// `split` CTAs.  The CTAs of a cluster take consecutive ranges of K; each holds a partial accumulator,
+// sends the columns that another CTA owns into that CTA's shared memory and sums its own in rank order, so
+// the result does not depend on timing and no workspace is needed.  Warp 0 issues the TMA copies (weights
+// as one box, tokens as 16-row boxes or, by the routing's indices, four rows at a time), warp 1 the MMAs; all
+// four warps store.  The tensor maps have two dimensions: boxes of a map with three or more came in at 10.6 TB/s
+// from L2 over the whole chip, those of a flat one at 16.9, and a TMA instruction costs about 100 cycles whatever its
+// size, so boxes are as high as the tile allows.  The tile of a cluster is found from the group offsets on the device.
 //
 // Every wait is bounded: one that runs out reports MOE_ERR_TIMEOUT, the copies in flight are waited
 // for, and the tensor memory is freed.
-#include <cuda_bf16.h>
-
 #include <atomic>
 
-#include "common.cuh"
-#include "ops.h"
-#include "tcgen05.cuh"
+#include "ragged.cuh"
 
 namespace moe {
 
 namespace ragged {
-constexpr int kRows = 128;       // weight rows per tile (MMA M)
-constexpr int kStageKBytes = 128;   // bytes of K per stage: one 128-byte swizzle row
-constexpr int kABytes = kRows * kStageKBytes;
-constexpr int kBoxRows = 16;     // token rows per TMA box
 constexpr int kMaxStages = 8;
 constexpr int kThreads = 128;
 constexpr int kTailBytes = 256;  // barriers, tile description
 }  // namespace ragged
 
-// D (+)= A * B^T, both operands in shared memory (K-major, 128-byte swizzle).
-__device__ __forceinline__ void umma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate)
-{
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-                 : "memory");
-}
-__device__ __forceinline__ void umma_i8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate)
-{
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-                 : "memory");
-}
-
-// Instruction descriptor of kind::i8: s32 accumulator (bits 4-5 = 2), signed A and B (bits 7-9 and
-// 10-12 = 1), both K-major, N >> 3 in bits 17-22, M >> 4 in bits 24-28.
-__device__ __forceinline__ uint32_t umma_idesc_i8(int m, int n)
-{
-    return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
-           (static_cast<uint32_t>(m >> 4) << 24);
-}
-
-// 5-D tiled copy of a weight box, and a gather of four rows of a 2-D map (box one row high).
-__device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, int c4,
-                                            uint64_t *bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
-        "[%1, {%2, %3, %4, %5, %6}], [%7];"
-        ::"r"(smem_u32(dst)), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar))
-        : "memory");
-}
+// A gather of four rows of a 2-D map (box one row high).
 __device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *map, int c0, const int (&r)[4], uint64_t *bar)
 {
     asm volatile(
@@ -83,98 +43,6 @@ __device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *map, i
         "[%1, {%2, %3, %4, %5, %6}], [%7];"
         ::"r"(smem_u32(dst)), "l"(map), "r"(c0), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(smem_u32(bar))
         : "memory");
-}
-
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void st_cluster(uint32_t smem_addr, uint32_t rank, uint32_t v)
-{
-    uint32_t remote;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr), "r"(rank));
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(v) : "memory");
-}
-
-// clamp-SwiGLU that lets a NaN through (a comparison with NaN is false).
-__device__ __forceinline__ float ragged_swiglu(float g, float u)
-{
-    const float a = g > 7.0f ? 7.0f : g;
-    const float c = u > 7.0f ? 7.0f : (u < -7.0f ? -7.0f : u);
-    return a / (1.0f + expf(-a)) * c;
-}
-
-// One value of the product, final: scaled (int8), rounded to the output's type and stored.
-template <bool kInt8>
-__device__ __forceinline__ void ragged_store(const RaggedArgs &a, float v, size_t row, int n)
-{
-    const size_t at = row * static_cast<size_t>(a.N) + n;
-    if (kInt8 && a.add != nullptr) v += __bfloat162float(a.add[at]);
-    if (a.y_f32)
-        static_cast<float *>(a.y)[at] = v;
-    else
-        static_cast<__nv_bfloat16 *>(a.y)[at] = __float2bfloat16_rn(v);
-}
-
-// The tt-th token tile of the groups, found by one warp: lanes take E / 32 consecutive groups each.
-// Offsets are clamped to [0, R] and to ascending order, so wrong ones cannot lead out of the tensors.
-__device__ __forceinline__ bool find_tile(const int32_t *off, int R, int E, int nt, int tt, int &expert, int &p0,
-                                          int &count)
-{
-    const int lane = threadIdx.x & 31;
-    if (off == nullptr) {
-        expert = 0;
-        p0 = tt * nt;
-        count = min(nt, R - p0);
-        return count > 0;
-    }
-    const int per = (E + 31) >> 5, e0 = lane * per, e1 = min(E, e0 + per);
-    int mine = 0;
-    int lo = e0 < E ? min(max(__ldcg(off + e0), 0), R) : 0;
-    const int lo0 = lo;
-#pragma unroll 8
-    for (int e = e0; e < e1; ++e) {
-        const int hi = min(max(__ldcg(off + e + 1), lo), R);
-        mine += (hi - lo + nt - 1) / nt;
-        lo = hi;
-    }
-    int incl = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += v;
-    }
-    const bool here = tt >= incl - mine && tt < incl;
-    const uint32_t who = __ballot_sync(0xffffffffu, here);
-    if (who == 0) return false;
-    int fe = 0, fp = 0, fc = 0;
-    if (here) {
-        int t = tt - (incl - mine);
-        lo = lo0;
-        for (int e = e0; e < e1; ++e) {
-            const int hi = min(max(__ldcg(off + e + 1), lo), R);
-            const int n = (hi - lo + nt - 1) / nt;
-            if (t < n) {
-                fe = e;
-                fp = lo + t * nt;
-                fc = min(nt, hi - fp);
-                break;
-            }
-            t -= n;
-            lo = hi;
-        }
-    }
-    const int src = __ffs(who) - 1;
-    expert = __shfl_sync(0xffffffffu, fe, src);
-    p0 = __shfl_sync(0xffffffffu, fp, src);
-    count = __shfl_sync(0xffffffffu, fc, src);
-    return true;
 }
 
 template <bool kInt8, bool kGather, bool kSwiglu>
@@ -193,6 +61,8 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     uint64_t *done = empty + kMaxStages;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
     volatile int *tile = reinterpret_cast<volatile int *>(tmem_slot + 2);   // found, expert, p0, count
+    float *rs = reinterpret_cast<float *>(smem + a.stages * stage_bytes + kTailBytes);   // [nt], int8
+    int *lo = reinterpret_cast<int *>(rs + a.nt), *first = lo + a.E + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const StatusPtrs status{nullptr, a.status_out};
@@ -214,19 +84,19 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         }
         mbar_init(done, 1);
         fence_barrier_init();
+        tile[0] = 0;
     }
     pdl_wait();
-    if (warp == 0) {
-        int e = 0, p = 0, c = 0;
-        const bool found = find_tile(a.offsets, a.R, a.E, a.nt, tt, e, p, c);
-        if (lane == 0) {
-            tile[0] = found;
+    tc_fence_before();
+    build_groups(a.offsets, a.R, a.E, a.nt, lo, first);
+    for (int e = threadIdx.x; e < a.E; e += kThreads)
+        if (first[e] <= tt && tt < first[e + 1]) {
+            const int rows = tile_rows(lo[e + 1] - lo[e], a.nt), p = lo[e] + (tt - first[e]) * rows;
+            tile[0] = 1;
             tile[1] = e;
             tile[2] = p;
-            tile[3] = c;
+            tile[3] = min(rows, lo[e + 1] - p);
         }
-    }
-    tc_fence_before();
     __syncthreads();
     tc_fence_after();
     pdl_trigger();
@@ -252,7 +122,10 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                         idx[h][i] = static_cast<int>(min(f / static_cast<uint32_t>(a.k), static_cast<uint32_t>(a.M - 1)));
                     }
             }
-            const uint32_t bytes = kABytes + (kGather ? groups * 4 : n16) * kStageKBytes;
+            const int boxes = (n16 + a.box_rows - 1) / a.box_rows;
+            const uint32_t bytes = kABytes + (kGather ? groups * 4 : boxes * a.box_rows) * kStageKBytes;
+            // rows past the expert's last come from the next one, or are zeros: nobody stores their products
+            const int wrow = kSwiglu ? expert * 2 * a.N + rb * 64 : expert * a.N + rb * kRows;
             int it = 0;
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int s = it % a.stages;
@@ -262,8 +135,12 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 uint8_t *sa = smem + s * stage_bytes, *sb = sa + kABytes;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&full[s], bytes);
-                    tma_load_5d(sa, &wmap, kb * kStageK, kSwiglu ? 0 : rb * kRows, 0, kSwiglu ? rb * 4 : 0, expert,
-                                &full[s]);
+                    if (kSwiglu) {   // 64 gate rows, then their 64 up rows
+                        tma_load_2d(sa, &wmap, kb * kStageK, wrow, &full[s]);
+                        tma_load_2d(sa + kABytes / 2, &wmap, kb * kStageK, wrow + a.N, &full[s]);
+                    } else {
+                        tma_load_2d(sa, &wmap, kb * kStageK, wrow, &full[s]);
+                    }
                 }
                 __syncwarp();
                 if (kGather) {
@@ -271,8 +148,8 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                     for (int h = 0; h < 2; ++h)
                         if (lane + 32 * h < groups)
                             tma_gather4(sb + (lane + 32 * h) * 4 * kStageKBytes, &xmap, kb * kStageK, idx[h], &full[s]);
-                } else if (lane < n16 / kBoxRows) {
-                    tma_load_2d(sb + lane * kBoxRows * kStageKBytes, &xmap, kb * kStageK, p0 + lane * kBoxRows,
+                } else if (lane < boxes) {
+                    tma_load_2d(sb + lane * a.box_rows * kStageKBytes, &xmap, kb * kStageK, p0 + lane * a.box_rows,
                                 &full[s]);
                 }
                 __syncwarp();
@@ -297,96 +174,85 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 const uint64_t ad = umma_sdesc_sw128(sa), bd = umma_sdesc_sw128(sa + kABytes);
                 if (elect_one()) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {   // 32 bytes of K each
-                        if (kInt8)
-                            umma_i8_ss(tmem, ad + 2 * j, bd + 2 * j, idesc, it > 0 || j > 0);
-                        else
-                            umma_f16_ss(tmem, ad + 2 * j, bd + 2 * j, idesc, it > 0 || j > 0);
-                    }
+                    for (int j = 0; j < 4; ++j)   // 32 bytes of K each
+                        umma_ss<kInt8, 1>(tmem, ad + 2 * j, bd + 2 * j, idesc, it > 0 || j > 0);
                     umma_commit(smem_u32(&empty[s]));
                 }
                 __syncwarp();
             }
             if (elect_one()) umma_commit(smem_u32(done));
             __syncwarp();
+        } else if (kInt8) {
+            for (int i = threadIdx.x - 64; i < n16; i += 64) rs[i] = i < count ? a.row_scale[p0 + i] : 0.f;
         }
         __syncwarp();
         // every MMA of this CTA has completed: the accumulator is whole, the stages are free
         mbar_wait_drain(done, 0, status);
+        if (kInt8) __syncthreads();   // rs
         tc_fence_after();
 
         // ------------------------------------------------------------ epilogue
-        // this thread's weight row is TMEM lane 32 * warp + lane
+        // this thread's accumulator row is TMEM lane 32 * warp + lane
         const uint32_t acc = tmem + (static_cast<uint32_t>(32 * warp) << 16);
-        const int n = kSwiglu ? rb * 64 + 16 * warp + (lane & 15) : rb * kRows + 32 * warp + lane;
-        const bool n_ok = n < a.N;
-        const float cs = kInt8 && n_ok ? a.col_scale[n] : 1.0f;
-        // the value of column c (of the two columns c, c + 1 when kSwiglu: gate rows sit in lanes 0..15,
-        // their up rows in lanes 16..31; the lower half finishes column c, the upper half c + 1)
-        auto finish = [&](uint32_t b0, uint32_t b1, int c, int cols) {
-            if (kSwiglu) {
-                const float v0 = __uint_as_float(b0), v1 = __uint_as_float(b1);
-                const bool up = lane >= 16;
-                const float other = __shfl_xor_sync(0xffffffffu, up ? v0 : v1, 16);
-                const float h = up ? ragged_swiglu(other, v1) : ragged_swiglu(v0, other);
-                const int col = c + (up ? 1 : 0);
-                if (n_ok && col < cols) ragged_store<false>(a, h, static_cast<size_t>(p0) + col, n);
-            } else {
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int col = c + q;
-                    if (!n_ok || col >= cols) continue;
-                    const uint32_t b = q == 0 ? b0 : b1;
-                    const size_t row = static_cast<size_t>(p0) + col;
-                    float v;
-                    if (kInt8)
-                        v = static_cast<float>(static_cast<int32_t>(b)) * a.row_scale[row] * cs;
-                    else
-                        v = __uint_as_float(b);
-                    ragged_store<kInt8>(a, v, row, n);
-                }
-            }
-        };
-        if (split == 1) {
+        const int n = rb * kRows + 32 * warp + lane;
+        const float cs = kInt8 && n < a.N ? a.col_scale[n] : 1.0f;
+        if (!kSwiglu && split == 1) {
             for (int c = 0; c < n16; c += 16) {
                 uint32_t v[16];
                 tmem_ld16(acc + c, v);
-#pragma unroll
-                for (int j = 0; j < 16; j += 2) finish(v[j], v[j + 1], c + j, count);
+                finish_columns<kInt8, 16>(a, v, rs + c, cs, static_cast<size_t>(p0) + c, count - c, n);
             }
         } else {
-            // rank r owns columns [r * own, (r + 1) * own); `own` is even, for the column pairs
+            // The accumulators go through shared memory, over the stages: [split][own][128] words in the CTA that
+            // owns the columns (rank r: r * own ..).  With one CTA, for the sake of SwiGLU alone, whose gate rows
+            // are lanes 0..63 and up rows lanes 64..127.
             const int own = ((n16 + 2 * split - 1) / (2 * split)) * 2;
-            const uint32_t buf = smem_u32(smem);   // [split][own][128] words over the stages
-            cluster_sync();                        // every CTA's MMAs are done with its stages
+            const uint32_t buf = smem_u32(smem);
+            if (split > 1)
+                cluster_sync();   // every CTA's MMAs are done with its stages
+            else
+                __syncthreads();
             for (int c = 0; c < n16; c += 16) {
                 uint32_t v[16];
                 tmem_ld16(acc + c, v);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    const int to = (c + j) / own, lc = (c + j) - to * own;
-                    st_cluster(buf + ((rank * own + lc) * kRows + 32 * warp + lane) * 4, to, v[j]);
+                    const int to = split > 1 ? (c + j) / own : 0, lc = (c + j) - to * own;
+                    const uint32_t at = buf + ((rank * own + lc) * kRows + 32 * warp + lane) * 4;
+                    if (split > 1)
+                        st_cluster(map_cluster(at, to), v[j]);
+                    else
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(v[j]) : "memory");
                 }
             }
-            cluster_sync();
-            const uint32_t *part = reinterpret_cast<const uint32_t *>(smem) + 32 * warp + lane;
-            for (int lc = 0; lc < own; lc += 2) {
-                const int c = rank * own + lc;
-                if (c >= count) break;   // warp-uniform
-                uint32_t s[2];
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    if (kInt8) {
-                        int32_t t = 0;
-                        for (int r = 0; r < split; ++r) t += static_cast<int32_t>(part[(r * own + lc + q) * kRows]);
-                        s[q] = static_cast<uint32_t>(t);
-                    } else {
-                        float t = 0.f;
-                        for (int r = 0; r < split; ++r) t += __uint_as_float(part[(r * own + lc + q) * kRows]);
-                        s[q] = __float_as_uint(t);
-                    }
+            if (split > 1)
+                cluster_sync();
+            else
+                __syncthreads();
+            const uint32_t *part = reinterpret_cast<const uint32_t *>(smem);
+            auto sum = [&](int lc, int r128) -> uint32_t {   // of the CTAs' parts, in rank order
+                const uint32_t *q = part + lc * kRows + r128;
+                if (kInt8) {
+                    int32_t t = 0;
+                    for (int r = 0; r < split; ++r) t += static_cast<int32_t>(q[r * own * kRows]);
+                    return static_cast<uint32_t>(t);
                 }
-                finish(s[0], s[1], c, count);
+                float t = 0.f;
+                for (int r = 0; r < split; ++r) t += __uint_as_float(q[r * own * kRows]);
+                return __float_as_uint(t);
+            };
+            const int mine = min(own, count - rank * own);   // of this CTA's columns, those of the tile
+            const size_t row0 = static_cast<size_t>(p0) + rank * own;
+            if (kSwiglu) {
+                const int r64 = threadIdx.x & 63, ns = rb * 64 + r64;
+                if (ns < a.N)
+                    for (int lc = threadIdx.x >> 6; lc < mine; lc += 2)
+                        store_pair(a, __uint_as_float(sum(lc, r64)), __uint_as_float(sum(lc, 64 + r64)), row0 + lc, ns);
+            } else {
+                for (int lc = 0; lc < mine; lc += 2) {
+                    const uint32_t v[2] = {sum(lc, 32 * warp + lane), sum(lc + 1, 32 * warp + lane)};
+                    finish_columns<kInt8, 2>(a, v, rs + rank * own + lc, cs, row0 + lc, mine - lc, n);
+                }
             }
         }
     }
@@ -397,21 +263,31 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
 
 // ------------------------------------------------------------------ launch
 
-RaggedPlan ragged_plan(int R, int N, int K, int E, bool int8, bool swiglu)
+RaggedPlan ragged_plan(int R, int N, int K, int E, bool int8, bool swiglu, bool gather)
 {
-    RaggedPlan p;
+    RaggedPlan p = {};
     const int avg = (R + E - 1) / E;
+    p.row_blocks = swiglu ? (N + 63) / 64 : (N + ragged::kRows - 1) / ragged::kRows;
+    p.kblocks = (K * (int8 ? 1 : 2) + ragged::kStageKBytes - 1) / ragged::kStageKBytes;
+    const long long pair_tiles = static_cast<long long>(E == 1 ? (R + 255) / 256 : (R < E ? R : E) + R / 256) *
+                                 ((p.row_blocks + 1) / 2);
+    p.wide = avg >= (E == 1 ? 128 : 32) && pair_tiles >= kPlanSMs / 2;
+    if (p.wide) {
+        p.nt = 256;
+        p.split = 1;
+        wide_plan(p, E, gather);
+        return p;
+    }
     // widest token tile; MMAs and copies follow the group's own size, so this only sets the stage size
     if (E == 1)
         p.nt = avg <= 32 ? 32 : (avg <= 64 ? 64 : (avg <= 128 ? 128 : 256));
     else
         p.nt = avg <= 8 ? 32 : (avg <= 32 ? 64 : (avg <= 96 ? 128 : 256));
+    p.box_rows = p.nt / 2;
     p.stages = p.nt == 32 ? 5 : (p.nt == 128 ? 6 : 4);
-    p.smem = 1024 + p.stages * (ragged::kABytes + p.nt * ragged::kStageKBytes) + ragged::kTailBytes;
-    p.row_blocks = swiglu ? (N + 63) / 64 : (N + ragged::kRows - 1) / ragged::kRows;
-    p.kblocks = (K * (int8 ? 1 : 2) + ragged::kStageKBytes - 1) / ragged::kStageKBytes;
-    p.max_tiles = (R < E ? R : E) + R / p.nt;
-    if (E == 1) p.max_tiles = (R + p.nt - 1) / p.nt;
+    p.smem = 1024 + p.stages * (ragged::kABytes + p.nt * ragged::kStageKBytes) + ragged::kTailBytes + p.nt * 4 +
+             2 * (E + 1) * 4;
+    p.max_tiles = E == 1 ? (R + p.nt - 1) / p.nt : (R < E ? R : E) + R / p.nt;
     const long long units = static_cast<long long>(p.max_tiles) * p.row_blocks;
     const int want = 2 * kPlanSMs;
     p.split = 1;

@@ -328,7 +328,7 @@ int moe_int8_gemm(const int8_t *q, const float *q_s, const int8_t *w_q, const fl
  * and the expert e whose range expert_offsets[e] .. expert_offsets[e+1]-1 holds p
  *   y[p] = w[e] x[row(p)]                                   (w bf16 [E,N,K])
  *   y[p] = silu(min(g,7)) * clamp(u,-7,7), [g;u] = w[e] x[row(p)]   (swiglu: w bf16 [E,2N,K], gate rows
- *                                                            0..N-1 then up rows; N a multiple of 16)
+ *                                                            0..N-1 then up rows)
  * row(p) = sorted_ids[p] / k with x bf16 [M,K] (the routed gather), or p with x bf16 [M*k,K] when
  * sorted_ids is NULL.  expert_offsets int32 [E+1] and sorted_ids int32 [M*k] as moe_permute writes them;
  * offsets ascend within 0..M*k.  Positions outside every range are left as they were in y.

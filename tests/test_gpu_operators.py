@@ -169,7 +169,8 @@ def int8_ref(q, qs, w, ws):
 
 INT8_SHAPES = [(1, 8, 16), (1, 1, 16), (1, 4096, 7168), (2, 1000, 528), (16, 128, 128), (17, 129, 144), (31, 512, 2048),
                (33, 1536, 2048), (64, 256, 4096), (65, 200, 1040), (100, 640, 512), (129, 96, 256), (200, 1024, 768),
-               (256, 128, 1024), (257, 384, 2048), (513, 2056, 400), (1000, 4096, 1536)]
+               (256, 128, 1024), (257, 384, 2048), (513, 2056, 400), (1000, 4096, 1536),
+               (2100, 2700, 272), (1500, 4100, 2000), (5000, 1000, 1024)]
 
 
 @pytest.mark.parametrize("M,N,K", INT8_SHAPES)
@@ -254,7 +255,9 @@ GROUPED_SHAPES = [
     (5, 3, 7, 1040, 1000, "skew"), (64, 4, 16, 256, 512, "uniform"), (64, 4, 16, 256, 512, "one"),
     (200, 2, 8, 384, 264, "skew"), (300, 4, 1000, 128, 256, "skew"), (257, 1, 3, 272, 520, "skew"),
     (129, 8, 8, 160, 136, "skew"), (700, 8, 16, 512, 1024, "uniform"), (1024, 8, 128, 256, 1536, "skew"),
-    (513, 4, 2, 1024, 2048, "skew"),
+    (513, 4, 2, 1024, 2048, "skew"), (1500, 2, 3, 1296, 200, "skew"), (700, 8, 32, 1536, 520, "uniform"),
+    (640, 8, 100, 1024, 1024, "skew"), (5000, 1, 1, 528, 1032, "uniform"),
+    (33, 2, 5, 77, 64, "uniform"), (5, 3, 7, 1001, 1000, "skew"), (2000, 1, 2, 2051, 136, "skew"),
 ]
 
 

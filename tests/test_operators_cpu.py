@@ -77,8 +77,7 @@ def test_grouped_refusals():
                dict(x=0x100008), dict(w=0x10000004), dict(y=0x400008), dict(off=0x200002), dict(ids=0x300001),
                dict(st=0x500002), dict(y=0x100000), dict(y=0x10000100), dict(y=0x200000), dict(y=0x300000 - 64)):
         assert gg(**kw) == INV, kw
-    for kw in (dict(K=1020), dict(K=65544), dict(N=65552), dict(E=1025), dict(k=33), dict(M=1 << 21),
-               dict(sw=1, N=520)):
+    for kw in (dict(K=1020), dict(K=65544), dict(N=65552), dict(E=1025), dict(k=33), dict(M=1 << 21)):
         assert gg(**kw) == UNS, kw
 
 
