@@ -58,7 +58,7 @@ struct RaggedArgs {
     int R, M, N, K, E, k;
     int nt, stages, row_blocks, kblocks, split, box_rows;
 };
-// Maps of the same rows with boxes of 16, 32, 64 and 128 of them.
+// Maps of the same rows with boxes of 16, 32, 64 and 128 of them; the first alone, one row high, for the gather.
 struct BoxMaps {
     CUtensorMap m[4];
 };

@@ -46,8 +46,8 @@ static int run_ragged(bool int8, bool swiglu, const void *w, uint64_t w_rows, Ra
     const uint64_t rows = static_cast<uint64_t>(a.M), K = static_cast<uint64_t>(a.K);
     if (p.wide) {
         BoxMaps maps = {};
-        for (int i = 0; i < 4 && !gather; ++i) {
-            rc = encode_rows_map(&maps.m[i], int8, a.x, rows, K, 16u << i);
+        for (int i = 0; i < (gather ? 1 : 4); ++i) {
+            rc = encode_rows_map(&maps.m[i], int8, a.x, rows, K, gather ? 1u : 16u << i);
             if (rc != MOE_OK) return rc;
         }
         if (a.status_out) {

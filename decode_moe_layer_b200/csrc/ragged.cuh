@@ -91,19 +91,24 @@ __device__ __forceinline__ void st_cluster(uint32_t cluster_addr, uint32_t v)
 
 // The groups of the rows, in shared memory: lo[e] is where group e starts (lo[E] where the last ends) and
 // first[e] the number of token tiles before it.  A group of c rows is cut into ceil(c / nt) tiles of equal
-// size rounded up to 16 rows, so that no tile is left with a few rows and a full price.
+// size rounded up to kStep rows (the MMA's N step), so that no tile is left with a few rows and a full price.
 // Whole CTA; `lo` and `first` hold E + 1 ints each.  Offsets are clamped to [0, R] and to ascending order, so
 // wrong ones cannot lead out of the tensors.  Returns after a barrier.
+template <int kStep>
 __device__ __forceinline__ int tile_rows(int c, int nt)
 {
+    if (c <= nt) return nt;
     const int t = (c + nt - 1) / nt;
-    return t <= 1 ? nt : ((c + t - 1) / t + 15) & ~15;
+    return ((c + t - 1) / t + kStep - 1) & ~(kStep - 1);
 }
+template <int kStep>
 __device__ __forceinline__ int tile_count(int c, int nt)
 {
-    const int rows = tile_rows(c, nt);
+    if (c <= nt) return c > 0;
+    const int rows = tile_rows<kStep>(c, nt);
     return (c + rows - 1) / rows;
 }
+template <int kStep>
 __device__ __forceinline__ void build_groups(const int32_t *off, int R, int E, int nt, int *lo, int *first)
 {
     if (off != nullptr) {
@@ -129,7 +134,7 @@ __device__ __forceinline__ void build_groups(const int32_t *off, int R, int E, i
         for (int e = e0; e < e1; ++e) lo[e] = before = max(before, lo[e]);
         __syncwarp();
         int mine = 0;
-        for (int e = e0; e < e1 && e < E; ++e) mine += tile_count(lo[e + 1] - lo[e], nt);
+        for (int e = e0; e < e1 && e < E; ++e) mine += tile_count<kStep>(lo[e + 1] - lo[e], nt);
         int incl = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -139,7 +144,7 @@ __device__ __forceinline__ void build_groups(const int32_t *off, int R, int E, i
         int at = incl - mine;
         for (int e = e0; e < e1; ++e) {
             first[e] = at;
-            if (e < E) at += tile_count(lo[e + 1] - lo[e], nt);
+            if (e < E) at += tile_count<kStep>(lo[e + 1] - lo[e], nt);
         }
     }
     __syncthreads();

@@ -45,6 +45,57 @@ __device__ __forceinline__ void tma_gather4(void *dst, const CUtensorMap *map, i
         : "memory");
 }
 
+// The tt-th token tile of the groups, found by one warp: lanes take ceil(E / 32) consecutive groups each.  A
+// group of c rows is cut as in build_groups.  Offsets are clamped to [0, R], so wrong ones cannot lead out of
+// the tensors.
+__device__ __forceinline__ bool find_tile(const int32_t *off, int R, int E, int nt, int tt, int &expert, int &p0,
+                                          int &count)
+{
+    const int lane = threadIdx.x & 31;
+    const int per = (E + 31) >> 5, e0 = lane * per, e1 = min(E, e0 + per);
+    auto at = [&](int e) { return off != nullptr ? min(max(__ldcg(off + e), 0), R) : (e == 0 ? 0 : R); };
+    int mine = 0;
+    const int lo0 = e0 < E ? at(e0) : 0;
+    int lo = lo0;
+#pragma unroll 8
+    for (int e = e0; e < e1; ++e) {
+        const int hi = max(at(e + 1), lo);
+        mine += tile_count<16>(hi - lo, nt);
+        lo = hi;
+    }
+    int incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += v;
+    }
+    const bool here = tt >= incl - mine && tt < incl;
+    const uint32_t who = __ballot_sync(0xffffffffu, here);
+    if (who == 0) return false;
+    int fe = 0, fp = 0, fc = 0;
+    if (here) {
+        int t = tt - (incl - mine);
+        lo = lo0;
+        for (int e = e0; e < e1; ++e) {
+            const int hi = max(at(e + 1), lo), n = tile_count<16>(hi - lo, nt);
+            if (t < n) {
+                const int rows = tile_rows<16>(hi - lo, nt);
+                fe = e;
+                fp = lo + t * rows;
+                fc = min(rows, hi - fp);
+                break;
+            }
+            t -= n;
+            lo = hi;
+        }
+    }
+    const int src = __ffs(who) - 1;
+    expert = __shfl_sync(0xffffffffu, fe, src);
+    p0 = __shfl_sync(0xffffffffu, fp, src);
+    count = __shfl_sync(0xffffffffu, fc, src);
+    return true;
+}
+
 template <bool kInt8, bool kGather, bool kSwiglu>
 __global__ void __launch_bounds__(ragged::kThreads)
 ragged_gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
@@ -62,7 +113,6 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
     volatile int *tile = reinterpret_cast<volatile int *>(tmem_slot + 2);   // found, expert, p0, count
     float *rs = reinterpret_cast<float *>(smem + a.stages * stage_bytes + kTailBytes);   // [nt], int8
-    int *lo = reinterpret_cast<int *>(rs + a.nt), *first = lo + a.E + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const StatusPtrs status{nullptr, a.status_out};
@@ -84,19 +134,19 @@ ragged_gemm_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         }
         mbar_init(done, 1);
         fence_barrier_init();
-        tile[0] = 0;
     }
     pdl_wait();
-    tc_fence_before();
-    build_groups(a.offsets, a.R, a.E, a.nt, lo, first);
-    for (int e = threadIdx.x; e < a.E; e += kThreads)
-        if (first[e] <= tt && tt < first[e + 1]) {
-            const int rows = tile_rows(lo[e + 1] - lo[e], a.nt), p = lo[e] + (tt - first[e]) * rows;
-            tile[0] = 1;
+    if (warp == 0) {
+        int e = 0, p = 0, c = 0;
+        const bool ok = find_tile(a.offsets, a.R, a.E, a.nt, tt, e, p, c);
+        if (lane == 0) {
+            tile[0] = ok;
             tile[1] = e;
             tile[2] = p;
-            tile[3] = min(rows, lo[e + 1] - p);
+            tile[3] = c;
         }
+    }
+    tc_fence_before();
     __syncthreads();
     tc_fence_after();
     pdl_trigger();
@@ -285,8 +335,7 @@ RaggedPlan ragged_plan(int R, int N, int K, int E, bool int8, bool swiglu, bool 
         p.nt = avg <= 8 ? 32 : (avg <= 32 ? 64 : (avg <= 96 ? 128 : 256));
     p.box_rows = p.nt / 2;
     p.stages = p.nt == 32 ? 5 : (p.nt == 128 ? 6 : 4);
-    p.smem = 1024 + p.stages * (ragged::kABytes + p.nt * ragged::kStageKBytes) + ragged::kTailBytes + p.nt * 4 +
-             2 * (E + 1) * 4;
+    p.smem = 1024 + p.stages * (ragged::kABytes + p.nt * ragged::kStageKBytes) + ragged::kTailBytes + p.nt * 4;
     p.max_tiles = E == 1 ? (R + p.nt - 1) / p.nt : (R < E ? R : E) + R / p.nt;
     const long long units = static_cast<long long>(p.max_tiles) * p.row_blocks;
     const int want = 2 * kPlanSMs;

@@ -10,8 +10,10 @@
 //     report to the even CTA's barrier.
 //   * warp 1 (even CTA): the MMAs; its commits release the stage in both CTAs.
 //   * warps 4..7: the epilogue of the CTA's 128 rows.
-//   * warps 8..11 (gather): token rows by the routing's indices with cp.async, written in the swizzled layout.
-//     TMA's four-row gather took 47 cycles an instruction here, 1500 a stage of 128 rows against the MMAs' 512.
+//   * warps 8..15 (gather): token rows by the routing's indices, four rows an instruction.  A warp issues such
+//     an instruction every 50 cycles or so (its operands differ by lane), so eight warps share a stage's 32; one
+//     warp took 1500 cycles over them against the MMAs' 512.  (cp.async in the swizzled layout was slower,
+//     830 cycles a stage: too few copies in flight.)
 // Tiles go round-robin over the clusters: experts in order, for each its blocks of weight rows, for each its
 // token tiles, so the tiles that run together share operands in L2.
 #include <atomic>
@@ -30,7 +32,7 @@ constexpr int kOffBars = kPipe * kPipeBytes;
 constexpr int kOffScales = kOffBars + 256;                // [2][kNt] fp32 row scales (int8)
 constexpr int kOffGroups = kOffScales + 8192;             // or, swiglu, what gate and up warps exchange: 8 KB
 constexpr int kTmemCols = 512;
-constexpr int kEpi0 = 4, kGather0 = 8, kGatherWarps = 4;
+constexpr int kEpi0 = 4, kGather0 = 8, kGatherWarps = 8;
 static_assert(2 * kNt * 4 <= 8192 && 2 * 4 * 8 * 32 * 4 <= 8192, "either fits");
 }  // namespace rwide
 
@@ -41,6 +43,15 @@ __device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *m
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
         "[%1, {%2, %3}], [%4];"
         ::"r"(smem_u32(dst)), "l"(map), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_gather4_pair(void *dst, const CUtensorMap *map, int c0, const int (&r)[4],
+                                                 uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
+        "[%1, {%2, %3, %4, %5, %6}], [%7];"
+        ::"r"(smem_u32(dst)), "l"(map), "r"(c0), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar)
         : "memory");
 }
 // One arrival on the barrier at the same place in both CTAs once the MMAs issued before are complete.
@@ -80,12 +91,6 @@ __device__ __forceinline__ void mbar_wait_cluster(uint64_t *bar, uint32_t parity
     }
 }
 
-// 16 bytes global -> shared, zeros where !live.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-}
-
 // The tiles of one cluster, in order: t = cluster, cluster + clusters, ...
 struct TileWalk {
     const int *lo, *first;
@@ -101,7 +106,7 @@ struct TileWalk {
         while (t >= first[e + 1] * pair_blocks) ++e;
         const int tiles = first[e + 1] - first[e], local = t - first[e] * pair_blocks;
         rb = local / tiles;
-        const int rows = tile_rows(lo[e + 1] - lo[e], rwide::kNt);
+        const int rows = tile_rows<32>(lo[e + 1] - lo[e], rwide::kNt);
         p0 = lo[e] + (local - rb * tiles) * rows;
         count = min(rows, lo[e + 1] - p0);
         return true;
@@ -110,7 +115,7 @@ struct TileWalk {
 };
 
 template <bool kInt8, bool kGather, bool kSwiglu>
-__global__ void __launch_bounds__(kGather ? 384 : 256, 1)
+__global__ void __launch_bounds__(kGather ? 32 * (rwide::kGather0 + rwide::kGatherWarps) : 256, 1)
 ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ BoxMaps xmaps,
                    const __grid_constant__ RaggedArgs a)
 {
@@ -135,8 +140,7 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
 
     if (warp == 0 && lane == 0) {
         prefetch_tensormap(&wmap);
-        if (!kGather)
-            for (int i = 0; i < 4; ++i) prefetch_tensormap(&xmaps.m[i]);
+        for (int i = 0; i < (kGather ? 1 : 4); ++i) prefetch_tensormap(&xmaps.m[i]);
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
@@ -146,7 +150,7 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     }
     if (threadIdx.x == 64) {
         for (int s = 0; s < kPipe; ++s) {
-            mbar_init(&full[s], kGather ? 3 : 1);   // the TMA copies; a gather warp of each CTA
+            mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -156,7 +160,7 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         fence_barrier_init();
     }
     pdl_wait();
-    build_groups(a.offsets, a.R, a.E, kNt, lo, first);
+    build_groups<32>(a.offsets, a.R, a.E, kNt, lo, first);
     tc_fence_before();
     __syncwarp();
     cluster_sync();   // barriers, tensor memory and tables of both CTAs are ready
@@ -176,7 +180,7 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             const int block = 2 * w.rb + static_cast<int>(rank);
             // weight rows past the expert's last come from the next one, or are zeros: nobody stores their products
             const int wrow = kSwiglu ? w.e * 2 * a.N + block * 64 : w.e * a.N + block * kRows;
-            const uint32_t bytes = 2 * (kABytes + (kGather ? 0 : (16 << box) * kStageKBytes));   // of both CTAs
+            const uint32_t bytes = 2 * (kABytes + (kGather ? half : 16 << box) * kStageKBytes);   // of both CTAs
             for (int kb = 0; kb < a.kblocks; ++kb, ++it) {
                 const int s = it % kPipe;
                 mbar_wait(&empty[s], ((it / kPipe) & 1) ^ 1, aborted, status);
@@ -287,44 +291,32 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         }
     } else if (kGather && warp >= kGather0) {
         // ------------------------------------------------------------ gather
-        // Warp g fills every fourth stage alone: its fence waits for all of its own copies, so stages in
-        // flight are as many as there are warps.  Lanes: row lane / 8 + 4 i, 16-byte piece lane % 8.
-        const int g = warp - kGather0, r0 = lane >> 3, piece = lane & 7;
-        const uint8_t *x = static_cast<const uint8_t *>(a.x);
-        const size_t pitch = static_cast<size_t>(a.K) * 2;
+        // Runs of four rows go round the warps, lane i of warp g taking run g + 8 i.
+        const int g = warp - kGather0;
         int it = 0;
         for (; w.locate(); w.next()) {
-            const int half = ((w.count + 31) & ~31) >> 1, runs = half >> 2;
-            int src[32];   // rows of x
+            const int half = ((w.count + 31) & ~31) >> 1;
+            const int run = g + kGatherWarps * lane;
+            const bool mine = 4 * run < half;
+            int idx[4];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const int r = min(static_cast<int>(rank) * half + r0 + 4 * i, w.count - 1);
-                const uint32_t f = static_cast<uint32_t>(__ldcg(a.sorted_ids + w.p0 + r));
-                src[i] = static_cast<int>(min(f / static_cast<uint32_t>(a.k), static_cast<uint32_t>(a.M - 1)));
+            for (int i = 0; i < 4; ++i) {
+                const int r = min(static_cast<int>(rank) * half + 4 * run + i, w.count - 1);
+                const uint32_t f = mine ? static_cast<uint32_t>(__ldcg(a.sorted_ids + w.p0 + r)) : 0u;
+                idx[i] = static_cast<int>(min(f / static_cast<uint32_t>(a.k), static_cast<uint32_t>(a.M - 1)));
             }
             for (int kb = 0; kb < a.kblocks; ++kb, ++it) {
-                if ((it & (kGatherWarps - 1)) != g) continue;
                 const int s = it % kPipe;
                 mbar_wait(&empty[s], ((it / kPipe) & 1) ^ 1, aborted, status);
                 aborted = __any_sync(0xffffffffu, aborted);
                 if (aborted) break;
-                const uint32_t sb = smem_u32(smem + s * kPipeBytes + kABytes) + r0 * kStageKBytes;
-                const size_t at = static_cast<size_t>(kb) * kStageKBytes + piece * 16;
-                const bool live = at < pitch;
-                const uint8_t *base = x + (live ? at : 0);
-                // row r0 + 4 i: r0 < 4, so its place in the 8-row swizzle alternates between two
-                const uint32_t d0 = sb + ((piece ^ r0) << 4), d1 = sb + ((piece ^ (r0 + 4)) << 4);
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (i < runs) cp_async16((i & 1 ? d1 : d0) + i * 4 * kStageKBytes, base + pitch * src[i], live);
-                asm volatile("cp.async.wait_all;" ::: "memory");
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                if (mine)
+                    tma_gather4_pair(smem + s * kPipeBytes + kABytes + run * 4 * kStageKBytes, &xmaps.m[0], kb * kStageK,
+                                     idx, map_cluster(smem_u32(&full[s]), 0));
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(map_cluster(smem_u32(&full[s]), 0));
             }
             if (aborted) break;
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
     }
     __syncwarp();
     tc_fence_before();
@@ -339,7 +331,7 @@ void wide_plan(RaggedPlan &p, int E, bool gather)
 {
     p.stages = rwide::kPipe;
     p.smem = 1024 + rwide::kOffGroups + 2 * (E + 1) * 4;
-    p.threads = gather ? 384 : 256;
+    p.threads = gather ? 32 * (rwide::kGather0 + rwide::kGatherWarps) : 256;
 }
 
 template <bool kInt8, bool kGather, bool kSwiglu>
