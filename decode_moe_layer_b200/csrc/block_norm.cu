@@ -11,6 +11,8 @@
 // codes need no reduction of their own: max|h| = rsqrt(..) * max|r' (w_pre + o)| comes with the second sum.
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "moe.h"
 #include "ops.h"
@@ -20,6 +22,10 @@ namespace moe {
 namespace norm {
 constexpr int kVec = 8;             // elements per 16-byte vector
 constexpr int kMaxThreads = 1024;
+constexpr int kRingThreads = 512;   // ring kernel: up to 4 vectors a thread
+constexpr int kMaxStages = 4;
+constexpr int kRingBytes = 200 * 1024;   // of an SM's shared memory, over its CTAs
+constexpr int kRingRows = 4 * kPlanSMs;  // from this many rows on
 }  // namespace norm
 
 __device__ __forceinline__ void unpack8(uint4 p, float (&f)[8])
@@ -83,81 +89,292 @@ __device__ __forceinline__ float2 block_sum_max(float sum, float mx, float2 *buf
     return make_float2(sum, mx);
 }
 
+// Few rows: a CTA per row, every piece loaded before the first reduction, so that a row costs one trip to memory.
 template <int V>
 __global__ void __launch_bounds__(norm::kMaxThreads) block_norm_kernel(const __grid_constant__ NormArgs a)
 {
     using norm::kVec;
     __shared__ float2 red[2][32];
-    const int nvec = a.H / kVec;
-    const float inv_h = 1.0f / static_cast<float>(a.H);
+    const int nvec = a.H / kVec, row = blockIdx.x;
+    const size_t base = static_cast<size_t>(row) * nvec;
     pdl_wait();
     pdl_trigger();
-    for (int row = blockIdx.x; row < a.M; row += gridDim.x) {
-        const size_t base = static_cast<size_t>(row) * nvec;
-        float v[V][8], r[V][8];
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    uint4 x[V], p[4][V];   // residual, gate, w_post, w_pre
+    const uint4 *src[4] = {reinterpret_cast<const uint4 *>(a.residual), nullptr,
+                           reinterpret_cast<const uint4 *>(a.w_post), reinterpret_cast<const uint4 *>(a.w_pre)};
+    if (a.residual != nullptr) src[0] += base;
+    if (a.gate_kind == MOE_GATE_FULL) src[1] = static_cast<const uint4 *>(a.gate) + base;
+    if (a.gate_kind == MOE_GATE_CHANNEL) src[1] = static_cast<const uint4 *>(a.gate);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        x[i] = c < nvec ? reinterpret_cast<const uint4 *>(a.x)[base + c] : zero;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) p[q][i] = src[q] != nullptr && c < nvec ? src[q][c] : zero;
+    }
+    float v[V][8];
+#pragma unroll
+    for (int i = 0; i < V; ++i) unpack8(x[i], v[i]);
+    const float inv_h = 1.0f / static_cast<float>(a.H);
+    float scale = a.block_scale;
+    if (a.gate_kind == MOE_GATE_TOKEN) scale *= static_cast<const float *>(a.gate)[row];
+    if (a.w_post != nullptr) {
         float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+        scale *= rsqrtf(block_sum_max(ss, 0.f, red[0]).x * inv_h + a.eps);
+    }
+    float ss2 = 0.f, mx = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        if (c >= nvec) continue;
+        float t[8];
+        if (a.w_post != nullptr) {
+            unpack8(p[2][i], t);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] *= t[j] + a.w_offset;
+        }
+        if (a.gate_kind == MOE_GATE_CHANNEL || a.gate_kind == MOE_GATE_FULL) {
+            unpack8(p[1][i], t);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] *= t[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] *= scale;
+        if (a.residual != nullptr) {
+            unpack8(p[0][i], t);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = fmaf(a.residual_scale, t[j], v[i][j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss2 = fmaf(v[i][j], v[i][j], ss2);
+        if (a.res_out != nullptr) reinterpret_cast<uint4 *>(a.res_out)[base + c] = pack8(v[i]);
+        if (a.w_pre != nullptr) {
+            unpack8(p[3][i], t);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[i][j] *= t[j] + a.w_offset;
+                mx = fmaxf(mx, fabsf(v[i][j]));
+            }
+        }
+    }
+    if (a.w_pre == nullptr) return;
+    const float2 st = block_sum_max(ss2, mx, red[1]);
+    const float inv = rsqrtf(st.x * inv_h + a.eps);
+    const float qs = st.y * inv / 127.0f;
+    if (a.q_out != nullptr && threadIdx.x == 0) a.q_s[row] = qs;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        if (c >= nvec) continue;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] *= inv;
+        if (a.h_out != nullptr) reinterpret_cast<uint4 *>(a.h_out)[base + c] = pack8(v[i]);
+        if (a.q_out != nullptr) reinterpret_cast<uint2 *>(a.q_out)[base + c] = int8_codes8(v[i], qs);
+    }
+}
+
+// Two fp32 values in one register pair: sm_100's packed fp32 arithmetic, each half rounded as the scalar
+// instruction rounds it.
+struct f2 {
+    float x, y;
+};
+__device__ __forceinline__ uint64_t f2_bits(f2 v)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+    return r;
+}
+__device__ __forceinline__ f2 f2_of(uint64_t r)
+{
+    f2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
+    return v;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)));
+    return f2_of(r);
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)), "l"(f2_bits(c)));
+    return f2_of(r);
+}
+__device__ __forceinline__ void unpack8(uint4 p, f2 (&f)[4])
+{
+    const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = {__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)};
+}
+__device__ __forceinline__ uint4 pack8(const f2 (&f)[4])
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f[i].x, f[i].y);
+        w[i] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// bulk_load of rows that nobody reads again: first to leave L2 (1 to 8% off the ring kernel's time).
+__device__ __forceinline__ void bulk_load_once(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    uint64_t policy;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;"
+        ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
+// Many rows: a few CTAs per SM, each with its rows (blockIdx.x, + gridDim.x, ..) on their way through a ring of
+// shared-memory stages (bulk copies of x, residual and a per-element gate), so that loads never wait for a
+// reduction.  What is the same for every row stays in registers in fp32: f_post = block_scale * (w_post + o) *
+// channel gate and f_pre = w_pre + o.  With a CTA per row 16384 x 7168 took 340 us; with this ring and
+// packed weights taken apart for every row 175 us and 30 instructions an element, most of the issue slots.
+template <int V, bool kQuant, bool kFullGate>
+__global__ void __launch_bounds__(norm::kRingThreads)
+block_norm_ring_kernel(const __grid_constant__ NormArgs a, int stages)
+{
+    using norm::kVec;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ float2 red[2][32];
+    __shared__ uint64_t full[norm::kMaxStages];
+    const int nvec = a.H / kVec;
+    const float inv_h = 1.0f / static_cast<float>(a.H);
+    const uint32_t row_bytes = static_cast<uint32_t>(a.H) * 2;
+    const bool has_res = a.residual != nullptr, has_post = a.w_post != nullptr, has_pre = a.w_pre != nullptr;
+    const uint32_t inputs = 1 + has_res + kFullGate;
+    const uint32_t gate_at = (inputs - 1) * row_bytes;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+        fence_barrier_init();
+    }
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+    auto issue = [&](int s, int row) {   // thread 0
+        uint8_t *dst = ring + s * inputs * row_bytes;
+        const size_t at = static_cast<size_t>(row) * a.H;
+        mbar_arrive_expect_tx(&full[s], inputs * row_bytes);
+        bulk_load_once(dst, a.x + at, row_bytes, &full[s]);
+        if (has_res) bulk_load_once(dst + row_bytes, a.residual + at, row_bytes, &full[s]);
+        if (kFullGate) bulk_load_once(dst + gate_at, static_cast<const __nv_bfloat16 *>(a.gate) + at, row_bytes, &full[s]);
+    };
+    if (threadIdx.x == 0)
+        for (int s = 0; s < stages; ++s) {
+            const long long row = blockIdx.x + static_cast<long long>(s) * gridDim.x;
+            if (row < a.M) issue(s, static_cast<int>(row));
+        }
+    f2 f_post[V][4], f_pre[V][4];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        const bool in = c < nvec;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f_post[i][j] = {a.block_scale, a.block_scale};
+            f_pre[i][j] = {1.f, 1.f};
+        }
+        f2 t[4];
+        if (in && has_post) {
+            unpack8(reinterpret_cast<const uint4 *>(a.w_post)[c], t);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f_post[i][j] = mul2(f_post[i][j], {t[j].x + a.w_offset, t[j].y + a.w_offset});
+        }
+        if (in && a.gate_kind == MOE_GATE_CHANNEL) {
+            unpack8(static_cast<const uint4 *>(a.gate)[c], t);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f_post[i][j] = mul2(f_post[i][j], t[j]);
+        }
+        if (in && has_pre) {
+            unpack8(reinterpret_cast<const uint4 *>(a.w_pre)[c], t);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f_pre[i][j] = {t[j].x + a.w_offset, t[j].y + a.w_offset};
+        }
+    }
+    bool aborted = false;
+    const StatusPtrs status{nullptr, nullptr};
+    const f2 rs2 = {a.residual_scale, a.residual_scale};
+    int s = 0, parity = 0;
+    for (long long row = blockIdx.x; row < a.M; row += gridDim.x) {
+        const float tg = a.gate_kind == MOE_GATE_TOKEN ? static_cast<const float *>(a.gate)[row] : 1.0f;
+        mbar_wait(&full[s], parity, aborted, status);
+        const uint8_t *st = ring + s * inputs * row_bytes;
+        const size_t base = static_cast<size_t>(row) * nvec;
+        f2 v[V][4];
+        f2 ss = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = threadIdx.x + i * blockDim.x;
-            if (c < nvec) {
-                unpack8(reinterpret_cast<const uint4 *>(a.x)[base + c], v[i]);
-                if (a.residual != nullptr) unpack8(reinterpret_cast<const uint4 *>(a.residual)[base + c], r[i]);
+            unpack8(c < nvec ? reinterpret_cast<const uint4 *>(st)[c] : make_uint4(0u, 0u, 0u, 0u), v[i]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
-            }
+            for (int j = 0; j < 4; ++j) ss = fma2(v[i][j], v[i][j], ss);
         }
-        float scale = a.block_scale;
-        if (a.gate_kind == MOE_GATE_TOKEN) scale *= static_cast<const float *>(a.gate)[row];
-        if (a.w_post != nullptr) scale *= rsqrtf(block_sum_max(ss, 0.f, red[0]).x * inv_h + a.eps);
-        const size_t gbase = a.gate_kind == MOE_GATE_FULL ? base : 0;
-        float ss2 = 0.f, mx = 0.f;
+        float scale = tg;
+        if (has_post) scale *= rsqrtf(block_sum_max(ss.x + ss.y, 0.f, red[0]).x * inv_h + a.eps);
+        const f2 scale2 = {scale, scale};
+        ss = {0.f, 0.f};
+        float mx = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = threadIdx.x + i * blockDim.x;
             if (c >= nvec) continue;
-            float t[8];
-            if (a.w_post != nullptr) {
-                unpack8(reinterpret_cast<const uint4 *>(a.w_post)[c], t);
+            f2 t[4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] *= t[j] + a.w_offset;
+            for (int j = 0; j < 4; ++j) v[i][j] = mul2(mul2(v[i][j], f_post[i][j]), scale2);
+            if (kFullGate) {
+                unpack8(reinterpret_cast<const uint4 *>(st + gate_at)[c], t);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[i][j] = mul2(v[i][j], t[j]);
             }
-            if (a.gate_kind == MOE_GATE_CHANNEL || a.gate_kind == MOE_GATE_FULL) {
-                unpack8(reinterpret_cast<const uint4 *>(a.gate)[gbase + c], t);
+            if (has_res) {
+                unpack8(reinterpret_cast<const uint4 *>(st + row_bytes)[c], t);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] *= t[j];
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[i][j] *= scale;
-                if (a.residual != nullptr) v[i][j] = fmaf(a.residual_scale, r[i][j], v[i][j]);
-                ss2 = fmaf(v[i][j], v[i][j], ss2);
+                for (int j = 0; j < 4; ++j) v[i][j] = fma2(rs2, t[j], v[i][j]);
             }
             if (a.res_out != nullptr) reinterpret_cast<uint4 *>(a.res_out)[base + c] = pack8(v[i]);
-            if (a.w_pre != nullptr) {
-                unpack8(reinterpret_cast<const uint4 *>(a.w_pre)[c], t);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    v[i][j] *= t[j] + a.w_offset;
-                    mx = fmaxf(mx, fabsf(v[i][j]));
+            for (int j = 0; j < 4; ++j) {
+                ss = fma2(v[i][j], v[i][j], ss);
+                v[i][j] = mul2(v[i][j], f_pre[i][j]);
+                if (kQuant) mx = fmaxf(mx, fmaxf(fabsf(v[i][j].x), fabsf(v[i][j].y)));
+            }
+        }
+        if (has_pre) {
+            const float2 sum = block_sum_max(ss.x + ss.y, mx, red[1]);
+            const float inv = rsqrtf(sum.x * inv_h + a.eps);
+            const f2 inv2 = {inv, inv};
+            const float qs = sum.y * inv / 127.0f;
+            if (kQuant && threadIdx.x == 0) a.q_s[row] = qs;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int c = threadIdx.x + i * blockDim.x;
+                if (c >= nvec) continue;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[i][j] = mul2(v[i][j], inv2);
+                if (a.h_out != nullptr) reinterpret_cast<uint4 *>(a.h_out)[base + c] = pack8(v[i]);
+                if (kQuant) {
+                    const float f[8] = {v[i][0].x, v[i][0].y, v[i][1].x, v[i][1].y,
+                                        v[i][2].x, v[i][2].y, v[i][3].x, v[i][3].y};
+                    reinterpret_cast<uint2 *>(a.q_out)[base + c] = int8_codes8(f, qs);
                 }
             }
         }
-        if (a.w_pre == nullptr) {
-            __syncthreads();   // red[0] is free for the next row
-            continue;
-        }
-        const float2 st = block_sum_max(ss2, mx, red[1]);
-        const float inv = rsqrtf(st.x * inv_h + a.eps);
-        const float qs = st.y * inv / 127.0f;
-        if (a.q_out != nullptr && threadIdx.x == 0) a.q_s[row] = qs;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = threadIdx.x + i * blockDim.x;
-            if (c >= nvec) continue;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] *= inv;
-            if (a.h_out != nullptr) reinterpret_cast<uint4 *>(a.h_out)[base + c] = pack8(v[i]);
-            if (a.q_out != nullptr) reinterpret_cast<uint2 *>(a.q_out)[base + c] = int8_codes8(v[i], qs);
+        __syncthreads();   // the stage has been read, the sums too
+        const long long next = row + static_cast<long long>(stages) * gridDim.x;
+        if (threadIdx.x == 0 && next < a.M) issue(s, static_cast<int>(next));
+        if (++s == stages) {
+            s = 0;
+            parity ^= 1;
         }
     }
 }
@@ -207,21 +424,59 @@ int8_quantize_kernel(const __nv_bfloat16 *x, int8_t *q, float *q_s, int M, int K
 
 // ------------------------------------------------------------------ launch
 
-// Rows of up to 1024 vectors: a vector per thread; longer ones two.
 static int row_threads(int nvec, int v)
 {
     const int t = (nvec + v - 1) / v;
     return (t + 31) / 32 * 32;
 }
 
+template <int V, bool kQuant, bool kFullGate>
+static cudaError_t launch_ring_t(const NormArgs &a, int threads, cudaStream_t s)
+{
+    auto kernel = block_norm_ring_kernel<V, kQuant, kFullGate>;
+    static std::atomic<bool> ready[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, norm::kRingBytes);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) ready[dev].store(true, std::memory_order_release);
+    }
+    const int inputs = 1 + (a.residual != nullptr) + kFullGate;
+    const int stage = inputs * a.H * 2;
+    // CTAs per SM: what the registers of 512 (V = 4) or 1024 threads leave room for, with two stages each at least
+    int ctas = (V == 4 ? 512 : 1024) / threads;
+    if (ctas > 16) ctas = 16;
+    while (ctas > 1 && 2 * ctas * stage > norm::kRingBytes) --ctas;
+    int stages = norm::kRingBytes / (ctas * stage);
+    if (stages > norm::kMaxStages) stages = norm::kMaxStages;
+    const int most = num_sms() * ctas;
+    return launch_ex(kernel, dim3(a.M < most ? a.M : most), dim3(threads), static_cast<size_t>(stages) * stage, s, true,
+                     a, stages);
+}
+
+template <int V>
+static cudaError_t launch_ring(const NormArgs &a, int threads, cudaStream_t s)
+{
+    const bool full = a.gate_kind == MOE_GATE_FULL;
+    if (a.q_out != nullptr)
+        return full ? launch_ring_t<V, true, true>(a, threads, s) : launch_ring_t<V, true, false>(a, threads, s);
+    return full ? launch_ring_t<V, false, true>(a, threads, s) : launch_ring_t<V, false, false>(a, threads, s);
+}
+
 cudaError_t launch_block_norm(const NormArgs &a, cudaStream_t s)
 {
     const int nvec = a.H / norm::kVec;
+    if (a.M >= norm::kRingRows) {
+        // few threads with several vectors each: the reductions cost less, more CTAs hide them (16384 rows of 2048:
+        // 50 us with four vectors a thread, 62 with one)
+        return nvec <= 64 ? launch_ring<2>(a, row_threads(nvec, 2), s) : launch_ring<4>(a, row_threads(nvec, 4), s);
+    }
     const int v = nvec <= norm::kMaxThreads ? 1 : 2;
     const int threads = row_threads(nvec, v);
-    const int grid = a.M;
-    return v == 1 ? launch_ex(block_norm_kernel<1>, dim3(grid), dim3(threads), 0, s, true, a)
-                  : launch_ex(block_norm_kernel<2>, dim3(grid), dim3(threads), 0, s, true, a);
+    return v == 1 ? launch_ex(block_norm_kernel<1>, dim3(a.M), dim3(threads), 0, s, true, a)
+                  : launch_ex(block_norm_kernel<2>, dim3(a.M), dim3(threads), 0, s, true, a);
 }
 
 cudaError_t launch_int8_quantize(const __nv_bfloat16 *x, bool swiglu, int8_t *q, float *q_s, int M, int K,
