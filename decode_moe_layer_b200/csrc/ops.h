@@ -32,19 +32,17 @@ cudaError_t launch_int8_quantize(const __nv_bfloat16 *x, bool swiglu, int8_t *q,
 cudaError_t launch_combine_rows(const void *y, bool y_f32, const float *topk_w, const int32_t *inv_pos,
                                 const __nv_bfloat16 *add, __nv_bfloat16 *out, int M, int H, int k, cudaStream_t s);
 
-// How a ragged product is cut: tiles of 128 weight rows x up to nt tokens with K over `split` CTAs
-// (ragged_gemm.cu), or tiles of 256 x 256 on CTA pairs (wide, ragged_wide.cu).
+// Whether a ragged product streams weight rows by warps (ragged_rows.cu) instead of tiles (ragged_wide.cu).
+constexpr int kRowsMaxTokens = 4;   // int8
+bool ragged_by_rows(int R, int E, bool int8);
+
+// How the tiles of 256 weight rows x up to nt tokens are run: `clusters` clusters of `split` CTA pairs, each pair
+// with its range of K.
 struct RaggedPlan {
-    bool wide;
-    int nt, stages, smem;
-    int box_rows;              // token rows per TMA box (!wide)
+    int nt, split, clusters, stages, ring_bytes, smem, threads;
     int row_blocks, kblocks;   // of 128 weight rows (swiglu: 64 output columns), of 128 bytes of K
-    int max_tiles;             // !wide: upper bound of the token tiles of any offsets
-    int split;
-    int threads;               // wide
 };
-RaggedPlan ragged_plan(int R, int N, int K, int E, bool int8, bool swiglu, bool gather);
-void wide_plan(RaggedPlan &p, int E, bool gather);
+RaggedPlan wide_plan(int R, int N, int K, int E, bool int8, bool swiglu, bool gather);
 
 struct RaggedArgs {
     const int32_t *offsets;      // [E+1]; nullptr: one group of all R rows
@@ -56,16 +54,16 @@ struct RaggedArgs {
     int32_t *status_out;
     int y_f32;
     int R, M, N, K, E, k;
-    int nt, stages, row_blocks, kblocks, split, box_rows;
+    int nt, stages, row_blocks, kblocks, split, ring_bytes;   // ragged_wide.cu
 };
 // Maps of the same rows with boxes of 16, 32, 64 and 128 of them; the first alone, one row high, for the gather.
 struct BoxMaps {
     CUtensorMap m[4];
 };
-cudaError_t launch_ragged(bool int8, bool swiglu, const CUtensorMap &wmap, const CUtensorMap &xmap, const RaggedArgs &a,
-                          const RaggedPlan &p, cudaStream_t s);
 cudaError_t launch_ragged_wide(bool int8, bool swiglu, const CUtensorMap &wmap, const BoxMaps &xmaps,
                                const RaggedArgs &a, const RaggedPlan &p, cudaStream_t s);
+
+cudaError_t launch_ragged_rows(bool int8, bool swiglu, const void *w, const RaggedArgs &a, cudaStream_t s);
 
 // Map of a row-major [rows][K] matrix of 8-bit or bf16 elements: boxes of 128 bytes x box_rows, 128-byte
 // swizzle, zeros outside; MOE_OK or MOE_ERR_CUDA (api.cu).

@@ -31,38 +31,31 @@ static bool finite_f(float v) { return v - v == 0.0f; }
 // Maps and launch of a ragged product whose arguments have been checked: w [w_rows][K], x [a.M][K].
 static int run_ragged(bool int8, bool swiglu, const void *w, uint64_t w_rows, RaggedArgs &a, cudaStream_t stream)
 {
+    if (a.status_out) {
+        const cudaError_t e = cudaMemsetAsync(a.status_out, 0, sizeof(int32_t), stream);
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    if (ragged_by_rows(a.R, a.E, int8)) {
+        const cudaError_t e = launch_ragged_rows(int8, swiglu, w, a, stream);
+        return e == cudaSuccess ? MOE_OK : cuda_fail(e);
+    }
     const bool gather = a.sorted_ids != nullptr;
-    const RaggedPlan p = ragged_plan(a.R, a.N, a.K, a.E, int8, swiglu, gather);
+    const RaggedPlan p = wide_plan(a.R, a.N, a.K, a.E, int8, swiglu, gather);
     a.nt = p.nt;
     a.stages = p.stages;
-    a.box_rows = p.box_rows;
     a.row_blocks = p.row_blocks;
     a.kblocks = p.kblocks;
     a.split = p.split;
-    // weight boxes of 128 rows, or (swiglu) of 64 gate rows and of 64 up rows
+    a.ring_bytes = p.ring_bytes;
+    // weight boxes of 128 rows, or (swiglu) of 64 gate rows and of 64 up rows; token boxes of every height
     CUtensorMap wmap;
-    int rc = encode_rows_map(&wmap, int8, w, w_rows, static_cast<uint64_t>(a.K), swiglu ? 64 : 128);
-    if (rc != MOE_OK) return rc;
+    BoxMaps maps;
     const uint64_t rows = static_cast<uint64_t>(a.M), K = static_cast<uint64_t>(a.K);
-    if (p.wide) {
-        BoxMaps maps = {};
-        for (int i = 0; i < (gather ? 1 : 4); ++i) {
-            rc = encode_rows_map(&maps.m[i], int8, a.x, rows, K, gather ? 1u : 16u << i);
-            if (rc != MOE_OK) return rc;
-        }
-        if (a.status_out) {
-            const cudaError_t e = cudaMemsetAsync(a.status_out, 0, sizeof(int32_t), stream);
-            if (e != cudaSuccess) return cuda_fail(e);
-        }
-        const cudaError_t e = launch_ragged_wide(int8, swiglu, wmap, maps, a, p, stream);
-        return e == cudaSuccess ? MOE_OK : cuda_fail(e);
-    }
-    CUtensorMap xmap;   // one row high for the gather
-    rc = encode_rows_map(&xmap, int8, a.x, rows, K, gather ? 1u : static_cast<uint32_t>(p.box_rows));
+    int rc = encode_rows_map(&wmap, int8, w, w_rows, K, swiglu ? 64 : 128);
+    for (int i = 0; i < (gather ? 1 : 4) && rc == MOE_OK; ++i)
+        rc = encode_rows_map(&maps.m[i], int8, a.x, rows, K, gather ? 1u : 16u << i);
     if (rc != MOE_OK) return rc;
-    cudaError_t e = cudaSuccess;
-    if (a.status_out) e = cudaMemsetAsync(a.status_out, 0, sizeof(int32_t), stream);
-    if (e == cudaSuccess) e = launch_ragged(int8, swiglu, wmap, xmap, a, p, stream);
+    const cudaError_t e = launch_ragged_wide(int8, swiglu, wmap, maps, a, p, stream);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e);
 }
 

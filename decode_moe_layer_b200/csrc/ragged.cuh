@@ -1,5 +1,12 @@
-// ragged.cuh -- device helpers that the two kernels of the ragged products share (ragged_gemm.cu,
-// ragged_wide.cu): tcgen05 and TMA forms, the table of token tiles, the epilogue.
+// ragged.cuh -- what the kernels of the ragged products share: matrix products whose rows come in groups of any
+// size, bf16 expert weights with ragged groups of tokens (moe_grouped_gemm) and int8 weights with one group
+// (moe_int8_gemm):
+//
+//   y[p][n] = epilogue( sum_c w[e(p)][n][c] * x[row(p)][c] )
+//
+// For a token or a few, weight rows are streamed by warps (ragged_rows.cu); all else runs in tiles on tcgen05 by
+// pairs of CTAs (ragged_wide.cu), whose width follows the groups' sizes.  Here: tcgen05 and cluster forms, the
+// table of token tiles, the epilogue.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -26,42 +33,32 @@ __device__ __forceinline__ uint32_t umma_idesc_i8(int m, int n)
            (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-// D (+)= A * B^T over 32 bytes of K: kind::f16 (16 bf16 elements) or kind::i8 (32 int8 elements), one CTA or
-// the CTA pair (issued by the pair's even CTA; each CTA holds half of A's rows and half of B's).
-template <bool kInt8, int kCtas>
-__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                        uint32_t accumulate)
+// D (+)= A * B^T over 32 bytes of K by the CTA pair: kind::f16 (16 bf16 elements) or kind::i8 (32 int8 elements).
+// Issued by the pair's even CTA; each CTA holds half of A's rows and half of B's.
+template <bool kInt8>
+__device__ __forceinline__ void umma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate)
 {
-#define MOE_UMMA_SS(group, kind)                                                                  \
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"                                \
-                 "tcgen05.mma.cta_group::" group ".kind::" kind " [%0], %1, %2, %3, p;\n\t}" ::"r"( \
-                     d_tmem),                                                                     \
-                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)                            \
-                 : "memory")
-    if (kCtas == 1) {
-        if (kInt8)
-            MOE_UMMA_SS("1", "i8");
-        else
-            MOE_UMMA_SS("1", "f16");
-    } else {
-        if (kInt8)
-            MOE_UMMA_SS("2", "i8");
-        else
-            MOE_UMMA_SS("2", "f16");
-    }
-#undef MOE_UMMA_SS
+    if (kInt8)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+                     "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+                     : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+                     "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+                     : "memory");
 }
 
-// 16 consecutive columns of this thread's TMEM lane, without waiting for them (tmem_wait_ld).
-__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&v)[16])
+// 8 consecutive columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8])
 {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-                   "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]),
-                   "=r"(v[15])
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
                  : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // ------------------------------------------------------------------ clusters
 
@@ -82,37 +79,42 @@ __device__ __forceinline__ uint32_t map_cluster(uint32_t smem_addr, uint32_t ran
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr), "r"(rank));
     return remote;
 }
-__device__ __forceinline__ void st_cluster(uint32_t cluster_addr, uint32_t v)
+__device__ __forceinline__ void st_cluster4(uint32_t cluster_addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
+// Sum of two accumulator words.
+template <bool kInt8>
+__device__ __forceinline__ uint32_t ragged_add(uint32_t a, uint32_t b)
+{
+    return kInt8 ? a + b : __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
 }
 
 // ------------------------------------------------------------------ token tiles
 
 // The groups of the rows, in shared memory: lo[e] is where group e starts (lo[E] where the last ends) and
 // first[e] the number of token tiles before it.  A group of c rows is cut into ceil(c / nt) tiles of equal
-// size rounded up to kStep rows (the MMA's N step), so that no tile is left with a few rows and a full price.
+// size rounded up to 32 rows (the MMA's N step), so that no tile is left with a few rows and a full price.
 // Whole CTA; `lo` and `first` hold E + 1 ints each.  Offsets are clamped to [0, R] and to ascending order, so
 // wrong ones cannot lead out of the tensors.  Returns after a barrier.
-template <int kStep>
 __device__ __forceinline__ int tile_rows(int c, int nt)
 {
     if (c <= nt) return nt;
     const int t = (c + nt - 1) / nt;
-    return ((c + t - 1) / t + kStep - 1) & ~(kStep - 1);
+    return ((c + t - 1) / t + 31) & ~31;
 }
-template <int kStep>
 __device__ __forceinline__ int tile_count(int c, int nt)
 {
     if (c <= nt) return c > 0;
-    const int rows = tile_rows<kStep>(c, nt);
+    const int rows = tile_rows(c, nt);
     return (c + rows - 1) / rows;
 }
-template <int kStep>
 __device__ __forceinline__ void build_groups(const int32_t *off, int R, int E, int nt, int *lo, int *first)
 {
     if (off != nullptr) {
-        for (int e = threadIdx.x; e <= E; e += blockDim.x) lo[e] = min(max(__ldcg(off + e), 0), R);
+        for (int e = threadIdx.x; e <= E; e += blockDim.x) lo[e] = min(max(off[e], 0), R);
     } else if (threadIdx.x == 0) {
         lo[0] = 0;
         lo[1] = R;
@@ -134,7 +136,7 @@ __device__ __forceinline__ void build_groups(const int32_t *off, int R, int E, i
         for (int e = e0; e < e1; ++e) lo[e] = before = max(before, lo[e]);
         __syncwarp();
         int mine = 0;
-        for (int e = e0; e < e1 && e < E; ++e) mine += tile_count<kStep>(lo[e + 1] - lo[e], nt);
+        for (int e = e0; e < e1 && e < E; ++e) mine += tile_count(lo[e + 1] - lo[e], nt);
         int incl = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -144,7 +146,7 @@ __device__ __forceinline__ void build_groups(const int32_t *off, int R, int E, i
         int at = incl - mine;
         for (int e = e0; e < e1; ++e) {
             first[e] = at;
-            if (e < E) at += tile_count<kStep>(lo[e + 1] - lo[e], nt);
+            if (e < E) at += tile_count(lo[e + 1] - lo[e], nt);
         }
     }
     __syncthreads();

@@ -1,0 +1,205 @@
+// ragged_rows.cu -- the ragged products (ragged.cuh) for the smallest calls: a token or a few.
+//
+// ragged_rows_kernel: a warp streams weight rows with plain 16-byte loads against up to kT tokens of one group,
+// kW rows at a time (swiglu: a gate row and its up row), the next 16 to 32 loads of a lane always on their way while
+// it works on the last; products and sums on the ordinary pipes (fp32 FMA; dp4a into int32), a warp reduction at the
+// end of a row.  No tensor map, barrier, cluster or tensor memory: what a call of this size waits for is the launch,
+// one trip to memory and the stream of the weights; the tensor-core kernel's set-up costs it
+// 3 to 5 us more (int8, one token, weights out of L2: 1536 x 2048 1.9 against 7.3 us, 4096 x 7168 6.4 against 12).
+// With several groups a tile is one position of the grouped order, whose group a warp counts out of the offsets; rows
+// of the same group then read its weights from L2 again, which is why groups of more than a row or so go to the tiles (ragged_by_rows).
+// The order of the sums is fixed: lane, then the reduction tree.
+#include "ragged.cuh"
+
+namespace moe {
+
+namespace rrows {
+constexpr int kWarps = 4;
+// rows at a time and 512-byte runs of each in flight: tokens share the weights' registers
+constexpr int rows_of(bool int8, int t) { return int8 && t > 1 ? 4 : 2; }
+constexpr int runs_of(bool int8, int t) { return int8 && t > 1 ? 2 : 4; }
+constexpr int kWarpsPerSm = 16;   // aimed at
+}  // namespace rrows
+
+__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+
+// acc += dot product of 16 bytes of weights and of a token.
+__device__ __forceinline__ void dot16(float &acc, uint4 w, uint4 x)
+{
+    const uint32_t a[4] = {w.x, w.y, w.z, w.w}, b[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        acc = fmaf(bf16_lo(a[i]), bf16_lo(b[i]), acc);
+        acc = fmaf(bf16_hi(a[i]), bf16_hi(b[i]), acc);
+    }
+}
+__device__ __forceinline__ void dot16(int &acc, uint4 w, uint4 x)
+{
+    acc = __dp4a(static_cast<int>(w.x), static_cast<int>(x.x), acc);
+    acc = __dp4a(static_cast<int>(w.y), static_cast<int>(x.y), acc);
+    acc = __dp4a(static_cast<int>(w.z), static_cast<int>(x.z), acc);
+    acc = __dp4a(static_cast<int>(w.w), static_cast<int>(x.w), acc);
+}
+
+template <bool kInt8>
+struct RowAcc {
+    typedef float type;
+};
+template <>
+struct RowAcc<true> {
+    typedef int type;
+};
+
+// steps: kW-row steps per warp.
+template <bool kInt8, bool kSwiglu, int kT>
+__global__ void __launch_bounds__(32 * rrows::kWarps)
+ragged_rows_kernel(const void *wbase, const __grid_constant__ RaggedArgs a, int row_blocks, int steps)
+{
+    using namespace rrows;
+    typedef typename RowAcc<kInt8>::type Acc;
+    constexpr int kW = rows_of(kInt8, kT), kRuns = runs_of(kInt8, kT), kCols = kSwiglu ? 1 : kW;
+    static_assert(!kSwiglu || (kW == 2 && kT == 1), "a gate row and its up row");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rb = blockIdx.x % row_blocks, tt = blockIdx.x / row_blocks;
+    // the warp's steps: columns n_first, + n_next, .. below a.N
+    const int n_first = (rb * steps * kWarps + warp) * kCols, n_next = kWarps * kCols;
+    if (n_first >= a.N) return;
+    pdl_wait();
+    pdl_trigger();
+    int expert = 0, p0 = tt * kT, count = min(kT, a.R - p0);
+    if (a.offsets != nullptr) {
+        // position tt is in the group after those that end at or before it
+        int before = 0;
+        for (int e = lane; e < a.E; e += 32) before += a.offsets[e + 1] <= tt;
+        expert = static_cast<int>(__reduce_add_sync(0xffffffffu, before));
+        if (expert >= a.E || a.offsets[0] > tt) return;
+    }
+
+    const int pieces = a.K * (kInt8 ? 1 : 2) / 16;   // 16-byte pieces of a row
+    const uint4 *w0 = static_cast<const uint4 *>(wbase) +
+                      static_cast<size_t>(expert) * a.N * (kSwiglu ? 2 : 1) * pieces;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    uint4 v[kRuns][kW];
+    auto load = [&](int n, int c0) {   // rows n.. (the last one again past a.N), pieces c0 + 32 u
+#pragma unroll
+        for (int r = 0; r < kW; ++r) {
+            const size_t row = kSwiglu ? static_cast<size_t>(n) + (r ? a.N : 0) : min(n + r, a.N - 1);
+            const uint4 *src = w0 + row * pieces;
+#pragma unroll
+            for (int u = 0; u < kRuns; ++u) v[u][r] = c0 + 32 * u < pieces ? __ldcs(src + c0 + 32 * u) : zero;
+        }
+    };
+    load(n_first, lane);
+    const uint4 *x[kT];
+#pragma unroll
+    for (int t = 0; t < kT; ++t) {
+        const int p = p0 + min(t, count - 1);
+        size_t row = static_cast<size_t>(p);
+        if (a.sorted_ids != nullptr) {
+            const uint32_t f = static_cast<uint32_t>(a.sorted_ids[p]);
+            row = min(f / static_cast<uint32_t>(a.k), static_cast<uint32_t>(a.M - 1));
+        }
+        x[t] = static_cast<const uint4 *>(a.x) + row * pieces;
+    }
+    Acc acc[kW][kT] = {};
+    int n = n_first, c0 = lane, left = steps;
+    while (true) {
+        uint4 now[kRuns][kW];
+#pragma unroll
+        for (int u = 0; u < kRuns; ++u)
+#pragma unroll
+            for (int r = 0; r < kW; ++r) now[u][r] = v[u][r];
+        const int c = c0, at = n;
+        // (by the row's first piece, so that all lanes go on together)
+        c0 += 32 * kRuns;
+        const bool row_done = c0 - lane >= pieces;
+        if (row_done) {
+            c0 = lane;
+            n += n_next;
+            --left;
+        }
+        const bool more = left > 0 && n < a.N;
+        if (more) load(n, c0);
+#pragma unroll
+        for (int u = 0; u < kRuns; ++u) {
+#pragma unroll
+            for (int t = 0; t < kT; ++t) {
+                // (zeros for both past the end: a token's NaN times a weight that is not there adds nothing)
+                const uint4 xv = c + 32 * u < pieces ? x[t][c + 32 * u] : zero;
+#pragma unroll
+                for (int r = 0; r < kW; ++r) dot16(acc[r][t], now[u][r], xv);
+            }
+        }
+        if (row_done) {
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+                for (int r = 0; r < kW; ++r)
+#pragma unroll
+                    for (int t = 0; t < kT; ++t) acc[r][t] += __shfl_xor_sync(0xffffffffu, acc[r][t], d);
+            // every lane has every sum: lane kW * t + r (swiglu: 0) stores its own
+            if (kSwiglu) {
+                if (lane == 0)
+                    store_pair(a, static_cast<float>(acc[0][0]), static_cast<float>(acc[1][0]), static_cast<size_t>(p0), at);
+            } else {
+#pragma unroll
+                for (int t = 0; t < kT; ++t)
+#pragma unroll
+                    for (int r = 0; r < kW; ++r)
+                        if (lane == kW * t + r && t < count && at + r < a.N) {
+                            const size_t row = static_cast<size_t>(p0) + t, to = row * a.N + at + r;
+                            float f = static_cast<float>(acc[r][t]);
+                            if (kInt8) {
+                                f = f * a.row_scale[row] * a.col_scale[at + r];
+                                if (a.add != nullptr) f += __bfloat162float(a.add[to]);
+                            }
+                            if (a.y_f32)
+                                static_cast<float *>(a.y)[to] = f;
+                            else
+                                static_cast<__nv_bfloat16 *>(a.y)[to] = __float2bfloat16_rn(f);
+                        }
+            }
+#pragma unroll
+            for (int r = 0; r < kW; ++r)
+#pragma unroll
+                for (int t = 0; t < kT; ++t) acc[r][t] = 0;
+        }
+        if (!more) break;
+    }
+}
+
+// ------------------------------------------------------------------ launch
+
+// Measured on this part (times on the GPU, weights out of L2):
+//  * int8, 4096 x 7168: 1, 2, 4 tokens 6.4, 8.5, 9.8 us by rows against 12 by tiles; 8 tokens 11.3 against 12.1, and
+//    1536 x 2048 3.9 against 7.3, but 7168 x 2048 9.9 against 8.0.
+//  * grouped, by rows against tiles: 4 tokens x 8 of 128 experts (1536 x 2048) 33 and 40 us, 8 tokens 58 and 60,
+//    16 tokens 84 and 85, 24 tokens 108 and 101; 16 tokens x 8 of 256 experts (7168 x 2048) 418 and 438, 24 tokens
+//    592 and 585: rows of the same group begin to share a tile.
+bool ragged_by_rows(int R, int E, bool int8) { return int8 ? R <= kRowsMaxTokens : 3LL * R <= 2LL * E; }
+
+template <bool kInt8, bool kSwiglu, int kT>
+static cudaError_t launch_rows_t(const void *w, const RaggedArgs &a, cudaStream_t s)
+{
+    using namespace rrows;
+    const int tiles = a.offsets != nullptr ? a.R : (a.R + kT - 1) / kT;
+    const int cols = kSwiglu ? 1 : rows_of(kInt8, kT), units = (a.N + cols - 1) / cols;   // steps of a tile
+    const long long target = static_cast<long long>(kWarpsPerSm) * kPlanSMs;
+    long long steps = static_cast<long long>(tiles) * units / target;
+    steps = steps < 1 ? 1 : (steps > 8 ? 8 : steps);
+    const int row_blocks = static_cast<int>((units + kWarps * steps - 1) / (kWarps * steps));
+    return launch_ex(ragged_rows_kernel<kInt8, kSwiglu, kT>, dim3(static_cast<unsigned>(tiles) * row_blocks),
+                     dim3(32 * kWarps), 0, s, true, w, a, row_blocks, static_cast<int>(steps));
+}
+
+cudaError_t launch_ragged_rows(bool int8, bool swiglu, const void *w, const RaggedArgs &a, cudaStream_t s)
+{
+    if (int8) {
+        if (a.R == 1) return launch_rows_t<true, false, 1>(w, a, s);
+        return a.R == 2 ? launch_rows_t<true, false, 2>(w, a, s) : launch_rows_t<true, false, 4>(w, a, s);
+    }
+    return swiglu ? launch_rows_t<false, true, 1>(w, a, s) : launch_rows_t<false, false, 1>(w, a, s);
+}
+
+}  // namespace moe

@@ -1,6 +1,12 @@
-// ragged_wide.cu -- the ragged products (ragged_gemm.cu) for groups of many rows.
+// ragged_wide.cu -- the ragged products (ragged.cuh) in tiles on tcgen05, from a few rows per group up.
 //
-// ragged_wide_kernel: persistent, one cluster of two CTAs per pair of SMs.  A tile is 256 weight rows x up to
+// kind::f16 (bf16 products, fp32 sums) or kind::i8 (int8 products, int32 sums, exact), the accumulator in tensor
+// memory.  128 bytes of K, 64 bf16 or 128 int8 values, are one pipeline stage and four MMAs in either type, so
+// one kernel serves both.  The weight rows are the MMA's M side and the tokens its N side, whose width follows the
+// group: a group of one row costs little more than its weights' way in, and rows beyond a group reach only
+// accumulator columns that nobody stores.
+//
+// ragged_wide_kernel: one cluster of two CTAs per pair of SMs, persistent.  A tile is 256 weight rows x up to
 // 256 tokens of one group; the pair runs it as one tcgen05.mma.cta_group::2 of M = 256, N = the tile's tokens
 // rounded up to 32.  Each CTA holds its 128 weight rows and half of the tokens in shared memory (the pair's MMA
 // reads both halves), so a stage brings 32 KB into each SM instead of the 48 KB of a 128 x 256 tile, and the
@@ -14,6 +20,11 @@
 //     an instruction every 50 cycles or so (its operands differ by lane), so eight warps share a stage's 32; one
 //     warp took 1500 cycles over them against the MMAs' 512.  (cp.async in the swizzled layout was slower,
 //     830 cycles a stage: too few copies in flight.)
+// With few tiles, clusters of up to eight CTAs take one each, every pair of them a range of K; they join their sums
+// through distributed shared memory in a fixed order.
+// The tensor maps have two dimensions: boxes of a map with three or more came in at 10.6 TB/s from L2 over the whole
+// chip, those of a flat one at 16.9, and a TMA instruction costs about 100 cycles whatever its size, so boxes are as
+// high as the tile allows.
 // Tiles go round-robin over the clusters: experts in order, for each its blocks of weight rows, for each its
 // token tiles, so the tiles that run together share operands in L2.
 #include <atomic>
@@ -24,16 +35,19 @@ namespace moe {
 
 namespace rwide {
 using namespace ragged;
-constexpr int kPipe = 6;
+constexpr int kMaxPipe = 6;
 constexpr int kNt = 256;                                  // tokens per tile
 constexpr int kBBytes = kNt / 2 * kStageKBytes;           // a CTA's half of them
 constexpr int kPipeBytes = kABytes + kBBytes;
-constexpr int kOffBars = kPipe * kPipeBytes;
-constexpr int kOffScales = kOffBars + 256;                // [2][kNt] fp32 row scales (int8)
+// behind the stages
+constexpr int kOffScales = 256;                           // [2][kNt] fp32 row scales (int8)
 constexpr int kOffGroups = kOffScales + 8192;             // or, swiglu, what gate and up warps exchange: 8 KB
+static_assert(2 * kNt * 4 <= 8192 && 2 * 4 * 8 * 32 * 4 <= 8192, "either fits");
 constexpr int kTmemCols = 512;
 constexpr int kEpi0 = 4, kGather0 = 8, kGatherWarps = 8;
-static_assert(2 * kNt * 4 <= 8192 && 2 * 4 * 8 * 32 * 4 <= 8192, "either fits");
+// split: partial sums in runs of 8 columns x 128 rows
+constexpr int kRunBytes = 8 * kRows * 4;
+constexpr int kMaxSplit = 4;                              // pairs per cluster
 }  // namespace rwide
 
 // Copies that complete on a barrier of either CTA of the pair (bar: cluster address).
@@ -54,11 +68,11 @@ __device__ __forceinline__ void tma_gather4_pair(void *dst, const CUtensorMap *m
         ::"r"(smem_u32(dst)), "l"(map), "r"(c0), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar)
         : "memory");
 }
-// One arrival on the barrier at the same place in both CTAs once the MMAs issued before are complete.
-__device__ __forceinline__ void umma_commit_pair(uint32_t mbar_smem)
+// One arrival on the barrier at the same place in both CTAs of the pair once the MMAs issued before are complete.
+__device__ __forceinline__ void umma_commit_pair(uint32_t mbar_smem, uint32_t leader)
 {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                 ::"r"(mbar_smem), "h"(static_cast<uint16_t>(3)) : "memory");
+                 ::"r"(mbar_smem), "h"(static_cast<uint16_t>(3u << leader)) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr)
 {
@@ -91,13 +105,28 @@ __device__ __forceinline__ void mbar_wait_cluster(uint64_t *bar, uint32_t parity
     }
 }
 
+// Where a warp is in the ring of stages.
+struct Ring {
+    int n, s = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ explicit Ring(int stages) : n(stages) {}
+    __device__ __forceinline__ void next()
+    {
+        if (++s == n) {
+            s = 0;
+            parity ^= 1;
+        }
+    }
+};
+
 // The tiles of one cluster, in order: t = cluster, cluster + clusters, ...
 struct TileWalk {
     const int *lo, *first;
-    int pair_blocks, total, step, t, e;
+    int nt, pair_blocks, total, step, t, e;
     int rb, p0, count;   // of the current tile
-    __device__ __forceinline__ TileWalk(const int *lo_, const int *first_, int E, int pair_blocks_, int start, int step_)
-        : lo(lo_), first(first_), pair_blocks(pair_blocks_), total(first_[E] * pair_blocks_), step(step_), t(start), e(0)
+    __device__ __forceinline__ TileWalk(const int *lo_, const int *first_, const RaggedArgs &a, int start, int step_)
+        : lo(lo_), first(first_), nt(a.nt), pair_blocks((a.row_blocks + 1) >> 1), total(first_[a.E] * pair_blocks),
+          step(step_), t(start), e(0)
     {
     }
     __device__ __forceinline__ bool locate()
@@ -106,7 +135,7 @@ struct TileWalk {
         while (t >= first[e + 1] * pair_blocks) ++e;
         const int tiles = first[e + 1] - first[e], local = t - first[e] * pair_blocks;
         rb = local / tiles;
-        const int rows = tile_rows<32>(lo[e + 1] - lo[e], rwide::kNt);
+        const int rows = tile_rows(lo[e + 1] - lo[e], nt);
         p0 = lo[e] + (local - rb * tiles) * rows;
         count = min(rows, lo[e + 1] - p0);
         return true;
@@ -115,7 +144,7 @@ struct TileWalk {
 };
 
 template <bool kInt8, bool kGather, bool kSwiglu>
-__global__ void __launch_bounds__(kGather ? 32 * (rwide::kGather0 + rwide::kGatherWarps) : 256, 1)
+__global__ void __launch_bounds__(kGather ? 32 * (rwide::kGather0 + rwide::kGatherWarps) : 256, 2)
 ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ BoxMaps xmaps,
                    const __grid_constant__ RaggedArgs a)
 {
@@ -124,32 +153,36 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffBars);   // used in the even CTA
-    uint64_t *empty = full + kPipe;
-    uint64_t *acc_full = empty + kPipe;
-    uint64_t *acc_empty = acc_full + 2;                               // used in the even CTA
+    uint8_t *tail = smem + a.ring_bytes;
+    uint64_t *full = reinterpret_cast<uint64_t *>(tail);   // used in the pair's even CTA
+    uint64_t *empty = full + kMaxPipe;
+    uint64_t *acc_full = empty + kMaxPipe;
+    uint64_t *acc_empty = acc_full + 2;                    // used in the pair's even CTA
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
-    float *scales = reinterpret_cast<float *>(smem + kOffScales), *exchange = scales;
-    int *lo = reinterpret_cast<int *>(smem + kOffGroups), *first = lo + a.E + 1;
+    float *scales = reinterpret_cast<float *>(tail + kOffScales), *exchange = scales;
+    int *lo = reinterpret_cast<int *>(tail + kOffGroups), *first = lo + a.E + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const StatusPtrs status{nullptr, a.status_out};
-    const uint32_t rank = cluster_rank();
-    const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
-    const int pair_blocks = (a.row_blocks + 1) >> 1;
+    const int split = a.split;                             // pairs of the cluster: consecutive ranges of K
+    const uint32_t crank = cluster_rank(), leader = crank & ~1u;
+    const int half_id = static_cast<int>(crank & 1), slice = static_cast<int>(crank >> 1);
+    const int cluster = blockIdx.x / (2 * split), clusters = gridDim.x / (2 * split);
+    const uint32_t tmem_cols = split > 1 ? kNt : kTmemCols;   // one accumulator or two
+    const int kb0 = a.kblocks * slice / split, kb1 = a.kblocks * (slice + 1) / split;
 
     if (warp == 0 && lane == 0) {
         prefetch_tensormap(&wmap);
-        for (int i = 0; i < (kGather ? 1 : 4); ++i) prefetch_tensormap(&xmaps.m[i]);
+        prefetch_tensormap(&xmaps.m[0]);
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                     "r"(kTmemCols)
+                     "r"(tmem_cols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     if (threadIdx.x == 64) {
-        for (int s = 0; s < kPipe; ++s) {
+        for (int s = 0; s < a.stages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
@@ -160,36 +193,36 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         fence_barrier_init();
     }
     pdl_wait();
-    build_groups<32>(a.offsets, a.R, a.E, kNt, lo, first);
+    build_groups(a.offsets, a.R, a.E, a.nt, lo, first);
     tc_fence_before();
     __syncwarp();
-    cluster_sync();   // barriers, tensor memory and tables of both CTAs are ready
+    cluster_sync();   // barriers, tensor memory and tables of all CTAs are ready
     tc_fence_after();
     pdl_trigger();
     const uint32_t tmem = *tmem_slot;
     bool aborted = false;
-    TileWalk w(lo, first, a.E, pair_blocks, cluster, clusters);
+    TileWalk w(lo, first, a, cluster, clusters);
 
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
-        int it = 0;
+        Ring ring(a.stages);
+        int issued = 0;
         for (; w.locate(); w.next()) {
             // one box of 16, 32, 64 or 128 token rows
             const int half = ((w.count + 31) & ~31) >> 1, box = half <= 16 ? 0 : (half <= 32 ? 1 : (half <= 64 ? 2 : 3));
-            const int row0 = w.p0 + static_cast<int>(rank) * half;
-            const int block = 2 * w.rb + static_cast<int>(rank);
+            const int row0 = w.p0 + half_id * half;
+            const int block = 2 * w.rb + half_id;
             // weight rows past the expert's last come from the next one, or are zeros: nobody stores their products
             const int wrow = kSwiglu ? w.e * 2 * a.N + block * 64 : w.e * a.N + block * kRows;
             const uint32_t bytes = 2 * (kABytes + (kGather ? half : 16 << box) * kStageKBytes);   // of both CTAs
-            for (int kb = 0; kb < a.kblocks; ++kb, ++it) {
-                const int s = it % kPipe;
-                mbar_wait(&empty[s], ((it / kPipe) & 1) ^ 1, aborted, status);
+            for (int kb = kb0; kb < kb1; ++kb, ring.next(), ++issued) {
+                mbar_wait(&empty[ring.s], ring.parity ^ 1, aborted, status);
                 aborted = __any_sync(0xffffffffu, aborted);
                 if (aborted) break;
-                uint8_t *sa = smem + s * kPipeBytes;
-                const uint32_t bar = map_cluster(smem_u32(&full[s]), 0);
+                uint8_t *sa = smem + ring.s * kPipeBytes;
+                const uint32_t bar = map_cluster(smem_u32(&full[ring.s]), leader);
                 if (lane == 0) {
-                    if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+                    if (half_id == 0) mbar_arrive_expect_tx(&full[ring.s], bytes);
                     if (kSwiglu) {   // 64 gate rows, then their 64 up rows
                         tma_load_2d_pair(sa, &wmap, kb * kStageK, wrow, bar);
                         tma_load_2d_pair(sa + kABytes / 2, &wmap, kb * kStageK, wrow + a.N, bar);
@@ -202,46 +235,46 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             }
             if (aborted) break;
         }
-        // after a timeout the even CTA waits for both CTAs' copies in flight
-        if (aborted && rank == 0)
-            for (int i = 0; i < kPipe && i < it; ++i) {
-                const int j = it - 1 - i;
-                mbar_wait_drain(&full[j % kPipe], (j / kPipe) & 1, status);
+        // after a timeout the even CTA waits for both CTAs' copies in flight: the stages before the one it gave up on
+        if (aborted && half_id == 0)
+            for (int i = 0; i < a.stages && i < issued; ++i) {
+                const int back = issued - 1 - i;
+                mbar_wait_drain(&full[back % a.stages], (back / a.stages) & 1, status);
             }
-    } else if (warp == 1 && rank == 0) {
+    } else if (warp == 1 && half_id == 0) {
         // ------------------------------------------------------------ MMA issuer
-        int it = 0;
+        Ring ring(a.stages);
         for (int i = 0; w.locate(); w.next(), ++i) {
             const int b = i & 1, n32 = (w.count + 31) & ~31;
             const uint32_t idesc = kInt8 ? umma_idesc_i8(256, n32) : umma_idesc_bf16(256, n32);
             const uint32_t acc = tmem + b * kNt;
             mbar_wait_cluster(&acc_empty[b], ((i >> 1) & 1) ^ 1, aborted, status);
-            for (int kb = 0; kb < a.kblocks; ++kb, ++it) {
-                const int s = it % kPipe;
-                mbar_wait_cluster(&full[s], (it / kPipe) & 1, aborted, status);
+            for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
+                mbar_wait_cluster(&full[ring.s], ring.parity, aborted, status);
                 aborted = __any_sync(0xffffffffu, aborted);
                 if (aborted) break;
                 tc_fence_after();
-                const uint32_t sa = smem_u32(smem + s * kPipeBytes);
+                const uint32_t sa = smem_u32(smem + ring.s * kPipeBytes);
                 const uint64_t ad = umma_sdesc_sw128(sa), bd = umma_sdesc_sw128(sa + kABytes);
                 if (elect_one()) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        umma_ss<kInt8, 2>(acc, ad + 2 * j, bd + 2 * j, idesc, kb > 0 || j > 0);
-                    umma_commit_pair(smem_u32(&empty[s]));
+                        umma_pair<kInt8>(acc, ad + 2 * j, bd + 2 * j, idesc, kb > kb0 || j > 0);
+                    umma_commit_pair(smem_u32(&empty[ring.s]), leader);
                 }
                 __syncwarp();
             }
             if (aborted) break;
-            if (elect_one()) umma_commit_pair(smem_u32(&acc_full[b]));
+            if (elect_one()) umma_commit_pair(smem_u32(&acc_full[b]), leader);
             __syncwarp();
         }
-    } else if (warp >= kEpi0 && warp < kEpi0 + 4) {
+    } else if (warp >= kEpi0 && warp < kEpi0 + 4 && split == 1) {
         // ------------------------------------------------------------ epilogue
         const int q = warp - kEpi0;
+        int turn = 0;   // of the exchange buffers, over all tiles
         for (int i = 0; w.locate(); w.next(), ++i) {
             const int b = i & 1;
-            const int block = 2 * w.rb + static_cast<int>(rank);
+            const int block = 2 * w.rb + half_id;
             const int n = block * kRows + 32 * q + lane;
             float cs = 1.0f;
             float *rs = scales + b * kNt;
@@ -258,25 +291,22 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 // Gate rows are lanes 0..63 (warps q = 0, 1), their up rows lanes 64..127 (q = 2, 3).  Warps q and
                 // q ^ 2 exchange halves of 16 columns: the gate warp finishes the first 8, the up warp the others.
                 const int up = q >> 1, ns = block * 64 + 32 * (q & 1) + lane;
-                for (int c = 0; c < w.count; c += 16) {
+                for (int c = 0; c < w.count; c += 16, turn ^= 1) {
                     uint32_t v[16];
                     tmem_ld16(acc + c, v);
-                    float *ex = exchange + ((c >> 4) & 1) * 1024;
+                    float *ex = exchange + turn * 1024;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) ex[q * 256 + j * 32 + lane] = __uint_as_float(up ? v[j] : v[8 + j]);
                     asm volatile("bar.sync %0, 64;" ::"r"(2 + (q & 1)) : "memory");
-                    float h[8];
+                    uint32_t h[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const float other = ex[(q ^ 2) * 256 + j * 32 + lane];
                         const float own = __uint_as_float(up ? v[8 + j] : v[j]);
-                        h[j] = ragged_swiglu(up ? other : own, up ? own : other);
+                        h[j] = __float_as_uint(ragged_swiglu(up ? other : own, up ? own : other));
                     }
-                    uint32_t hb[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) hb[j] = __float_as_uint(h[j]);
                     const int c0 = c + 8 * up;
-                    finish_columns<false, 8>(a, hb, nullptr, 1.0f, static_cast<size_t>(w.p0) + c0, w.count - c0, ns);
+                    finish_columns<false, 8>(a, h, nullptr, 1.0f, static_cast<size_t>(w.p0) + c0, w.count - c0, ns);
                 }
             } else {
                 for (int c = 0; c < w.count; c += 16) {
@@ -287,13 +317,13 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_cluster(smem_u32(&acc_empty[b]), 0));
+            if (lane == 0) mbar_arrive_cluster(map_cluster(smem_u32(&acc_empty[b]), leader));
         }
     } else if (kGather && warp >= kGather0) {
         // ------------------------------------------------------------ gather
         // Runs of four rows go round the warps, lane i of warp g taking run g + 8 i.
         const int g = warp - kGather0;
-        int it = 0;
+        Ring ring(a.stages);
         for (; w.locate(); w.next()) {
             const int half = ((w.count + 31) & ~31) >> 1;
             const int run = g + kGatherWarps * lane;
@@ -301,37 +331,146 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             int idx[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int r = min(static_cast<int>(rank) * half + 4 * run + i, w.count - 1);
-                const uint32_t f = mine ? static_cast<uint32_t>(__ldcg(a.sorted_ids + w.p0 + r)) : 0u;
+                const int r = min(half_id * half + 4 * run + i, w.count - 1);
+                const uint32_t f = mine ? static_cast<uint32_t>(a.sorted_ids[w.p0 + r]) : 0u;
                 idx[i] = static_cast<int>(min(f / static_cast<uint32_t>(a.k), static_cast<uint32_t>(a.M - 1)));
             }
-            for (int kb = 0; kb < a.kblocks; ++kb, ++it) {
-                const int s = it % kPipe;
-                mbar_wait(&empty[s], ((it / kPipe) & 1) ^ 1, aborted, status);
+            for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
+                mbar_wait(&empty[ring.s], ring.parity ^ 1, aborted, status);
                 aborted = __any_sync(0xffffffffu, aborted);
                 if (aborted) break;
                 if (mine)
-                    tma_gather4_pair(smem + s * kPipeBytes + kABytes + run * 4 * kStageKBytes, &xmaps.m[0], kb * kStageK,
-                                     idx, map_cluster(smem_u32(&full[s]), 0));
+                    tma_gather4_pair(smem + ring.s * kPipeBytes + kABytes + run * 4 * kStageKBytes, &xmaps.m[0],
+                                     kb * kStageK, idx, map_cluster(smem_u32(&full[ring.s]), leader));
                 __syncwarp();
             }
             if (aborted) break;
+        }
+    }
+    if (split > 1) {
+        // ------------------------------------------------------------ joining the slices of K
+        // The cluster has one tile at most.  Runs of 8 columns go round the pairs: run u is summed and stored by the
+        // pair u % split, whose CTAs get the other slices' parts of it in shared memory, over the stages:
+        // [slice][run / split][column half][row][4].  All sums in slice order.
+        TileWalk t(lo, first, a, cluster, clusters);
+        const bool found = t.locate();
+        if (found) mbar_wait_cluster(&acc_full[0], 0, aborted, status);
+        tc_fence_after();
+        __syncwarp();
+        cluster_sync();   // every pair's MMAs are done with its stages
+        const int runs = found ? (t.count + 7) >> 3 : 0, own = (runs + split - 1) / split;
+        const int group = warp >> 2, row = 32 * (warp & 3) + lane;
+        if (warp < 8) {
+            const uint32_t acc = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+            for (int u = group; u < runs; u += 2) {
+                uint32_t v[8];
+                tmem_ld8(acc + 8 * u, v);
+                const int to = u % split;
+                const uint32_t at = map_cluster(smem_u32(smem) + (slice * own + u / split) * kRunBytes + row * 16,
+                                                static_cast<uint32_t>(2 * to + half_id));
+                st_cluster4(at, v[0], v[1], v[2], v[3]);
+                st_cluster4(at + kRunBytes / 2, v[4], v[5], v[6], v[7]);
+            }
+        }
+        __syncwarp();
+        cluster_sync();
+        if (warp < 8) {
+            const int block = 2 * t.rb + half_id;
+            const int n = block * kRows + row;
+            const float cs = kInt8 && found && n < a.N ? a.col_scale[n] : 1.0f;
+            // part of slice s for run i, column half h, accumulator row r
+            auto part = [&](int s, int i, int h, int r) {
+                return *reinterpret_cast<const uint4 *>(smem + (s * own + i) * kRunBytes + h * (kRunBytes / 2) + r * 16);
+            };
+            auto sum = [&](int i, int h, int r, uint32_t *out) {
+                uint4 p = part(0, i, h, r);
+                for (int s = 1; s < split; ++s) {
+                    const uint4 q = part(s, i, h, r);
+                    p.x = ragged_add<kInt8>(p.x, q.x);
+                    p.y = ragged_add<kInt8>(p.y, q.y);
+                    p.z = ragged_add<kInt8>(p.z, q.z);
+                    p.w = ragged_add<kInt8>(p.w, q.w);
+                }
+                out[0] = p.x;
+                out[1] = p.y;
+                out[2] = p.z;
+                out[3] = p.w;
+            };
+            for (int i = group; i * split + slice < runs; i += 2) {
+                const int c = 8 * (i * split + slice), live = t.count - c;
+                const size_t row0 = static_cast<size_t>(t.p0) + c;
+                if (kSwiglu) {   // two threads per output row, four columns each
+                    const int r = row & 63, h = row >> 6;
+                    uint32_t g[4], up[4], v[4];
+                    sum(i, h, r, g);
+                    sum(i, h, 64 + r, up);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        v[j] = __float_as_uint(ragged_swiglu(__uint_as_float(g[j]), __uint_as_float(up[j])));
+                    finish_columns<false, 4>(a, v, nullptr, 1.0f, row0 + 4 * h, live - 4 * h, block * 64 + r);
+                } else {
+                    uint32_t v[8];
+                    float rs[8];
+                    sum(i, 0, row, v);
+                    sum(i, 1, row, v + 4);
+                    if (kInt8)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) rs[j] = j < live ? a.row_scale[row0 + j] : 0.f;
+                    finish_columns<kInt8, 8>(a, v, rs, cs, row0, live, n);
+                }
+            }
         }
     }
     __syncwarp();
     tc_fence_before();
     cluster_sync();   // neither CTA ends while the other's MMAs read it or its arrivals are on their way
     if (warp == 1)
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(tmem_cols) : "memory");
 }
 
 // ------------------------------------------------------------------ launch
 
-void wide_plan(RaggedPlan &p, int E, bool gather)
+RaggedPlan wide_plan(int R, int N, int K, int E, bool int8, bool swiglu, bool gather)
 {
-    p.stages = rwide::kPipe;
-    p.smem = 1024 + rwide::kOffGroups + 2 * (E + 1) * 4;
-    p.threads = gather ? 32 * (rwide::kGather0 + rwide::kGatherWarps) : 256;
+    using namespace rwide;
+    RaggedPlan p = {};
+    p.row_blocks = swiglu ? (N + 63) / 64 : (N + kRows - 1) / kRows;
+    p.kblocks = (K * (int8 ? 1 : 2) + kStageKBytes - 1) / kStageKBytes;
+    const int pair_blocks = (p.row_blocks + 1) / 2;
+    const int least = E == 1 ? (R + kNt - 1) / kNt : (R < E ? R : E) + R / kNt;   // token tiles of up to 256
+    const int widest = R < kNt ? (R + 31) / 32 * 32 : kNt;
+    // Token tiles and pairs per cluster by the estimated cycles of the longest cluster: waves x stages x a stage (its
+    // bytes at 60 a cycle, or its MMAs), the last tile's columns (20 cycles each) and, if pairs share a tile, the
+    // joining (2500 and 40 a column).  More, narrower tiles than `least` only for a single group, whose size the host
+    // knows.  With up to three stages, and one accumulator, two CTAs share an SM; then 33 clusters of eight CTAs or
+    // 71 of four fit the chip, else 15 or 33.
+    // Measured (int8, 4096 x 7168, four pairs against one): 16 tokens 12.1 and 16.2 us; (7168 x 2048, two) 9.3 and 8.1.
+    long long best = -1;
+    for (int tokens = least; tokens == least || (E == 1 && tokens * pair_blocks <= kPlanSMs && tokens * 32 <= R + 31); ++tokens) {
+        const int nt = tokens == least ? widest : ((R + tokens - 1) / tokens + 31) / 32 * 32;
+        const int box = nt <= 32 ? 16 : (nt <= 64 ? 32 : (nt <= 128 ? 64 : 128));
+        const long long stage = kABytes + box * kStageKBytes, cycles = stage / 60 > 2 * nt ? stage / 60 : 2 * nt;
+        const long long tiles = static_cast<long long>(tokens) * pair_blocks;
+        for (int split = 1; split <= kMaxSplit; split *= 2) {
+            const int need = split > 1 ? split * ((nt / 8 + split - 1) / split) * kRunBytes : 0;   // partial sums
+            const bool twice = need <= 3 * kPipeBytes;
+            const int fit = split == 4 ? (twice ? 33 : 15) : (split == 2 ? (twice ? 71 : 33) : kPlanSMs / 2);
+            if (split > 1 && (tiles > fit || p.kblocks < 4 * split)) continue;
+            const int slice = (p.kblocks + split - 1) / split;
+            const long long cost = (tiles + fit - 1) / fit * slice * cycles + 20 * nt + (split > 1 ? 2500 + 40 * nt : 0);
+            if (best >= 0 && cost >= best) continue;
+            best = cost;
+            const int most = split > 1 && twice ? 3 : kMaxPipe;
+            p.split = split;
+            p.nt = tokens == least ? kNt : nt;
+            p.stages = split > 1 && slice < most ? slice : most;
+            p.ring_bytes = p.stages * kPipeBytes > need ? p.stages * kPipeBytes : need;
+            p.clusters = static_cast<int>(tiles < fit ? tiles : fit);
+        }
+    }
+    p.smem = 1024 + p.ring_bytes + kOffGroups + 2 * (E + 1) * 4;
+    p.threads = gather ? 32 * (kGather0 + kGatherWarps) : 256;
+    return p;
 }
 
 template <bool kInt8, bool kGather, bool kSwiglu>
@@ -349,7 +488,7 @@ static cudaError_t launch_wide_t(const CUtensorMap &wmap, const BoxMaps &xmaps, 
         if (dev < 64) ready[dev].store(true, std::memory_order_release);
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(num_sms() & ~1));
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * p.split * p.clusters));
     cfg.blockDim = dim3(p.threads);
     cfg.dynamicSmemBytes = p.smem;
     cfg.stream = s;
@@ -357,7 +496,7 @@ static cudaError_t launch_wide_t(const CUtensorMap &wmap, const BoxMaps &xmaps, 
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.x = 2 * p.split;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
