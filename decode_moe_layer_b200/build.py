@@ -1,4 +1,5 @@
-"""Build libmoe.so (in-tree, next to this file) from csrc/*.cu for sm_100a.
+"""Build libmoe.so (in-tree, next to this file) from csrc/*.cu for sm_100a, and _ops.so, the compiled half of the
+Python binding (csrc/python_ops.cpp, plain C++ against torch and libmoe.so).
 
     python decode_moe_layer_b200/build.py [--force] [--verbose]
 
@@ -13,11 +14,15 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe.so")
+BINDING_SRC = os.path.join(CSRC, "python_ops.cpp")
+BINDING = os.path.join(HERE, "_ops.so")
+CUDA_HOME = os.environ.get("CUDA_HOME", "/usr/local/cuda")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 NVCC_FLAGS = [
@@ -43,6 +48,31 @@ def _stale() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    lib = build_library(force, verbose)
+    build_binding(force)
+    return lib
+
+
+def build_binding(force: bool = False) -> str:
+    deps = [BINDING_SRC, os.path.join(ROOT, "include", "moe.h")]
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps):
+        return BINDING
+    import torch
+    base = os.path.dirname(torch.__file__)
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    subprocess.check_call(
+        ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-Wall",
+         "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch.compiled_with_cxx11_abi()),
+         "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(base, "include"),
+         "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+         "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(CUDA_HOME, "include"),
+         BINDING_SRC, "-o", tmp, "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
+         "-ltorch_cuda", "-lc10", "-lc10_cuda", "-L", HERE, "-lmoe", "-Wl,-rpath,$ORIGIN"])
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
         return LIB
     objdir = os.path.join(ROOT, "_build")
