@@ -39,7 +39,8 @@ bool ragged_by_rows(int R, int E, bool int8);
 // How the tiles of 256 weight rows x up to nt tokens are run: `clusters` clusters of `split` CTA pairs, each pair
 // with its range of K.
 struct RaggedPlan {
-    int nt, split, clusters, stages, ring_bytes, smem, threads;
+    int nt, split, clusters, stages, stage_bytes, ring_bytes, smem, threads;
+    int accs, acc_cols;        // accumulators and their columns of tensor memory
     int row_blocks, kblocks;   // of 128 weight rows (swiglu: 64 output columns), of 128 bytes of K
 };
 RaggedPlan wide_plan(int R, int N, int K, int E, bool int8, bool swiglu, bool gather);
@@ -54,7 +55,7 @@ struct RaggedArgs {
     int32_t *status_out;
     int y_f32;
     int R, M, N, K, E, k;
-    int nt, stages, row_blocks, kblocks, split, ring_bytes;   // ragged_wide.cu
+    int nt, stages, stage_bytes, row_blocks, kblocks, split, ring_bytes, accs, acc_cols;   // ragged_wide.cu
 };
 // Maps of the same rows with boxes of 16, 32, 64 and 128 of them; the first alone, one row high, for the gather.
 struct BoxMaps {

@@ -43,6 +43,9 @@ static int run_ragged(bool int8, bool swiglu, const void *w, uint64_t w_rows, Ra
     const RaggedPlan p = wide_plan(a.R, a.N, a.K, a.E, int8, swiglu, gather);
     a.nt = p.nt;
     a.stages = p.stages;
+    a.stage_bytes = p.stage_bytes;
+    a.accs = p.accs;
+    a.acc_cols = p.acc_cols;
     a.row_blocks = p.row_blocks;
     a.kblocks = p.kblocks;
     a.split = p.split;

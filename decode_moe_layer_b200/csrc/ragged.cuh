@@ -68,6 +68,12 @@ __device__ __forceinline__ uint32_t cluster_rank()
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
+// Without ordering memory: for the end of a kernel, where it only keeps CTAs alive (the ordering form waits until
+// the stores before it have arrived, 1000 cycles and more).
+__device__ __forceinline__ void cluster_sync_relaxed()
+{
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -97,8 +103,7 @@ __device__ __forceinline__ uint32_t ragged_add(uint32_t a, uint32_t b)
 // The groups of the rows, in shared memory: lo[e] is where group e starts (lo[E] where the last ends) and
 // first[e] the number of token tiles before it.  A group of c rows is cut into ceil(c / nt) tiles of equal
 // size rounded up to 32 rows (the MMA's N step), so that no tile is left with a few rows and a full price.
-// Whole CTA; `lo` and `first` hold E + 1 ints each.  Offsets are clamped to [0, R] and to ascending order, so
-// wrong ones cannot lead out of the tensors.  Returns after a barrier.
+// Offsets are clamped to [0, R] and to ascending order, so wrong ones cannot lead out of the tensors.
 __device__ __forceinline__ int tile_rows(int c, int nt)
 {
     if (c <= nt) return nt;
@@ -111,45 +116,46 @@ __device__ __forceinline__ int tile_count(int c, int nt)
     const int rows = tile_rows(c, nt);
     return (c + rows - 1) / rows;
 }
-__device__ __forceinline__ void build_groups(const int32_t *off, int R, int E, int nt, int *lo, int *first)
+// A scan over the CTA's kThreads threads, inclusive: op is addition or maximum.  `part` holds one value per warp;
+// the caller puts a barrier between two scans.
+template <int kThreads, typename Op>
+__device__ __forceinline__ int block_scan(int v, int *part, Op op)
 {
-    if (off != nullptr) {
-        for (int e = threadIdx.x; e <= E; e += blockDim.x) lo[e] = min(max(off[e], 0), R);
-    } else if (threadIdx.x == 0) {
-        lo[0] = 0;
-        lo[1] = R;
-    }
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        // lanes take `per` consecutive entries of lo: running maximum, then the tiles of their groups
-        const int lane = threadIdx.x, per = (E + 32) >> 5, e0 = lane * per, e1 = min(E + 1, e0 + per);
-        int m = 0;
-        for (int e = e0; e < e1; ++e) m = max(m, lo[e]);
-        int before = m;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, before, d);
-            if (lane >= d) before = max(before, v);
-        }
-        before = __shfl_up_sync(0xffffffffu, before, 1);
-        if (lane == 0) before = 0;
-        for (int e = e0; e < e1; ++e) lo[e] = before = max(before, lo[e]);
-        __syncwarp();
-        int mine = 0;
-        for (int e = e0; e < e1 && e < E; ++e) mine += tile_count(lo[e + 1] - lo[e], nt);
-        int incl = mine;
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v = op(v, o);
+    }
+    if (lane == 31) part[warp] = v;
+    __syncthreads();
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += v;
-        }
-        int at = incl - mine;
-        for (int e = e0; e < e1; ++e) {
-            first[e] = at;
-            if (e < E) at += tile_count(lo[e + 1] - lo[e], nt);
+    for (int w = 0; w < kThreads / 32 - 1; ++w)
+        if (w < warp) v = op(v, part[w]);
+    return v;
+}
+// The table by a whole CTA of kThreads threads; `lo` and `first` hold E + 1 ints each, `part` 64.  Ends with a barrier.
+template <int kThreads>
+__device__ __forceinline__ void build_groups(const int32_t *off, int R, int E, int nt, int *lo, int *first, int *part)
+{
+    int high = 0, tiles = 0;   // of the groups before this round's
+    for (int base = 0; base <= E; base += kThreads) {
+        const int e = base + static_cast<int>(threadIdx.x);
+        // where the group starts, not before any earlier one
+        const int at = e <= E ? min(max(off[e], 0), R) : 0;
+        const int start = max(high, block_scan<kThreads>(at, part, [](int a, int b) { return max(a, b); }));
+        if (e <= E) lo[e] = start;
+        __syncthreads();
+        // the group before e is whole now (entry base - 1 comes from the round before)
+        const int mine = e > 0 && e <= E ? tile_count(lo[e] - lo[e - 1], nt) : 0;
+        const int sum = tiles + block_scan<kThreads>(mine, part + 32, [](int a, int b) { return a + b; });
+        if (e <= E) first[e] = sum;
+        __syncthreads();
+        if (base + kThreads <= E) {
+            high = lo[base + kThreads - 1];
+            tiles = first[base + kThreads - 1];
         }
     }
-    __syncthreads();
 }
 
 // ------------------------------------------------------------------ epilogue

@@ -12,8 +12,8 @@
 // reads both halves), so a stage brings 32 KB into each SM instead of the 48 KB of a 128 x 256 tile, and the
 // accumulator of its 128 rows in its own tensor memory, twice (256 columns each), so that one tile's
 // epilogue overlaps the next tile's products.
-//   * warp 0 (both CTAs): TMA copies of its weight rows and, without the gather, its token rows; they
-//     report to the even CTA's barrier.
+//   * warps 0 and 2 (both CTAs): TMA copies of its weight rows and, without the gather, its token rows; they
+//     report to the even CTA's barrier.  (Issued by one warp they took 400 cycles a stage.)
 //   * warp 1 (even CTA): the MMAs; its commits release the stage in both CTAs.
 //   * warps 4..7: the epilogue of the CTA's 128 rows.
 //   * warps 8..15 (gather): token rows by the routing's indices, four rows an instruction.  A warp issues such
@@ -35,16 +35,16 @@ namespace moe {
 
 namespace rwide {
 using namespace ragged;
-constexpr int kMaxPipe = 6;
-constexpr int kNt = 256;                                  // tokens per tile
-constexpr int kBBytes = kNt / 2 * kStageKBytes;           // a CTA's half of them
-constexpr int kPipeBytes = kABytes + kBBytes;
+constexpr int kMaxPipe = 8;
+constexpr int kNt = 256;                                  // most tokens per tile
+constexpr int kMaxRingBytes = 6 * (kABytes + kNt / 2 * kStageKBytes);
+constexpr int kHalfSmBytes = 102 * 1024;                  // ring of a CTA that leaves room for another on its SM
 // behind the stages
-constexpr int kOffScales = 256;                           // [2][kNt] fp32 row scales (int8)
+constexpr int kOffScales = 512;                           // [2][kNt] fp32 row scales (int8)
 constexpr int kOffGroups = kOffScales + 8192;             // or, swiglu, what gate and up warps exchange: 8 KB
 static_assert(2 * kNt * 4 <= 8192 && 2 * 4 * 8 * 32 * 4 <= 8192, "either fits");
-constexpr int kTmemCols = 512;
 constexpr int kEpi0 = 4, kGather0 = 8, kGatherWarps = 8;
+constexpr int threads_of(bool gather) { return 32 * (gather ? kGather0 + kGatherWarps : kGather0); }
 // split: partial sums in runs of 8 columns x 128 rows
 constexpr int kRunBytes = 8 * kRows * 4;
 constexpr int kMaxSplit = 4;                              // pairs per cluster
@@ -105,6 +105,9 @@ __device__ __forceinline__ void mbar_wait_cluster(uint64_t *bar, uint32_t parity
     }
 }
 
+// The box that holds a CTA's half of a tile's tokens: 16 << box rows.
+__device__ __forceinline__ int box_of(int half) { return half <= 16 ? 0 : (half <= 32 ? 1 : (half <= 64 ? 2 : 3)); }
+
 // Where a warp is in the ring of stages.
 struct Ring {
     int n, s = 0;
@@ -144,12 +147,12 @@ struct TileWalk {
 };
 
 template <bool kInt8, bool kGather, bool kSwiglu>
-__global__ void __launch_bounds__(kGather ? 32 * (rwide::kGather0 + rwide::kGatherWarps) : 256, 2)
+__global__ void __launch_bounds__(rwide::threads_of(kGather), 2)
 ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ BoxMaps xmaps,
                    const __grid_constant__ RaggedArgs a)
 {
     using namespace rwide;
-    constexpr int kStageK = kInt8 ? 128 : 64;
+    constexpr int kStageK = kInt8 ? 128 : 64, kThreads = threads_of(kGather);
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -159,6 +162,7 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     uint64_t *acc_full = empty + kMaxPipe;
     uint64_t *acc_empty = acc_full + 2;                    // used in the pair's even CTA
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
+    int *part = reinterpret_cast<int *>(tail + 256);
     float *scales = reinterpret_cast<float *>(tail + kOffScales), *exchange = scales;
     int *lo = reinterpret_cast<int *>(tail + kOffGroups), *first = lo + a.E + 1;
 
@@ -168,7 +172,6 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     const uint32_t crank = cluster_rank(), leader = crank & ~1u;
     const int half_id = static_cast<int>(crank & 1), slice = static_cast<int>(crank >> 1);
     const int cluster = blockIdx.x / (2 * split), clusters = gridDim.x / (2 * split);
-    const uint32_t tmem_cols = split > 1 ? kNt : kTmemCols;   // one accumulator or two
     const int kb0 = a.kblocks * slice / split, kb1 = a.kblocks * (slice + 1) / split;
 
     if (warp == 0 && lane == 0) {
@@ -177,7 +180,7 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                     "r"(tmem_cols)
+                     "r"(a.accs * a.acc_cols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
@@ -192,44 +195,42 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         }
         fence_barrier_init();
     }
-    pdl_wait();
-    build_groups(a.offsets, a.R, a.E, a.nt, lo, first);
+    if (a.offsets == nullptr && threadIdx.x == 96) {   // one group
+        lo[0] = first[0] = 0;
+        lo[1] = a.R;
+        first[1] = tile_count(a.R, a.nt);
+    }
     tc_fence_before();
     __syncwarp();
-    cluster_sync();   // barriers, tensor memory and tables of all CTAs are ready
+    cluster_sync();   // barriers and tensor memory of all CTAs are ready
     tc_fence_after();
+    pdl_wait();
+    if (a.offsets != nullptr) build_groups<kThreads>(a.offsets, a.R, a.E, a.nt, lo, first, part);
     pdl_trigger();
     const uint32_t tmem = *tmem_slot;
     bool aborted = false;
     TileWalk w(lo, first, a, cluster, clusters);
 
     if (warp == 0) {
-        // ------------------------------------------------------------ TMA producer
+        // ------------------------------------------------------------ weights
         Ring ring(a.stages);
         int issued = 0;
         for (; w.locate(); w.next()) {
-            // one box of 16, 32, 64 or 128 token rows
-            const int half = ((w.count + 31) & ~31) >> 1, box = half <= 16 ? 0 : (half <= 32 ? 1 : (half <= 64 ? 2 : 3));
-            const int row0 = w.p0 + half_id * half;
-            const int block = 2 * w.rb + half_id;
+            const int half = ((w.count + 31) & ~31) >> 1, block = 2 * w.rb + half_id;
             // weight rows past the expert's last come from the next one, or are zeros: nobody stores their products
             const int wrow = kSwiglu ? w.e * 2 * a.N + block * 64 : w.e * a.N + block * kRows;
-            const uint32_t bytes = 2 * (kABytes + (kGather ? half : 16 << box) * kStageKBytes);   // of both CTAs
+            // of both CTAs, weights and tokens
+            const uint32_t bytes = 2 * (kABytes + (kGather ? half : 16 << box_of(half)) * kStageKBytes);
             for (int kb = kb0; kb < kb1; ++kb, ring.next(), ++issued) {
                 mbar_wait(&empty[ring.s], ring.parity ^ 1, aborted, status);
                 aborted = __any_sync(0xffffffffu, aborted);
                 if (aborted) break;
-                uint8_t *sa = smem + ring.s * kPipeBytes;
+                uint8_t *sa = smem + ring.s * a.stage_bytes;
                 const uint32_t bar = map_cluster(smem_u32(&full[ring.s]), leader);
-                if (lane == 0) {
+                if (elect_one()) {
                     if (half_id == 0) mbar_arrive_expect_tx(&full[ring.s], bytes);
-                    if (kSwiglu) {   // 64 gate rows, then their 64 up rows
-                        tma_load_2d_pair(sa, &wmap, kb * kStageK, wrow, bar);
-                        tma_load_2d_pair(sa + kABytes / 2, &wmap, kb * kStageK, wrow + a.N, bar);
-                    } else {
-                        tma_load_2d_pair(sa, &wmap, kb * kStageK, wrow, bar);
-                    }
-                    if (!kGather) tma_load_2d_pair(sa + kABytes, &xmaps.m[box], kb * kStageK, row0, bar);
+                    tma_load_2d_pair(sa, &wmap, kb * kStageK, wrow, bar);   // swiglu: 64 gate rows, then their up rows
+                    if (kSwiglu) tma_load_2d_pair(sa + kABytes / 2, &wmap, kb * kStageK, wrow + a.N, bar);
                 }
                 __syncwarp();
             }
@@ -241,20 +242,36 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 const int back = issued - 1 - i;
                 mbar_wait_drain(&full[back % a.stages], (back / a.stages) & 1, status);
             }
+    } else if (!kGather && warp == 2) {
+        // ------------------------------------------------------------ tokens: one box of 16, 32, 64 or 128 rows
+        Ring ring(a.stages);
+        for (; w.locate(); w.next()) {
+            const int half = ((w.count + 31) & ~31) >> 1, box = box_of(half), row0 = w.p0 + half_id * half;
+            for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
+                mbar_wait(&empty[ring.s], ring.parity ^ 1, aborted, status);
+                aborted = __any_sync(0xffffffffu, aborted);
+                if (aborted) break;
+                const uint32_t bar = map_cluster(smem_u32(&full[ring.s]), leader);
+                if (elect_one())
+                    tma_load_2d_pair(smem + ring.s * a.stage_bytes + kABytes, &xmaps.m[box], kb * kStageK, row0, bar);
+                __syncwarp();
+            }
+            if (aborted) break;
+        }
     } else if (warp == 1 && half_id == 0) {
         // ------------------------------------------------------------ MMA issuer
         Ring ring(a.stages);
         for (int i = 0; w.locate(); w.next(), ++i) {
-            const int b = i & 1, n32 = (w.count + 31) & ~31;
+            const int b = a.accs > 1 ? i & 1 : 0, n32 = (w.count + 31) & ~31;
             const uint32_t idesc = kInt8 ? umma_idesc_i8(256, n32) : umma_idesc_bf16(256, n32);
-            const uint32_t acc = tmem + b * kNt;
+            const uint32_t acc = tmem + b * a.acc_cols;
             mbar_wait_cluster(&acc_empty[b], ((i >> 1) & 1) ^ 1, aborted, status);
             for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
                 mbar_wait_cluster(&full[ring.s], ring.parity, aborted, status);
                 aborted = __any_sync(0xffffffffu, aborted);
                 if (aborted) break;
                 tc_fence_after();
-                const uint32_t sa = smem_u32(smem + ring.s * kPipeBytes);
+                const uint32_t sa = smem_u32(smem + ring.s * a.stage_bytes);
                 const uint64_t ad = umma_sdesc_sw128(sa), bd = umma_sdesc_sw128(sa + kABytes);
                 if (elect_one()) {
 #pragma unroll
@@ -273,7 +290,7 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         const int q = warp - kEpi0;
         int turn = 0;   // of the exchange buffers, over all tiles
         for (int i = 0; w.locate(); w.next(), ++i) {
-            const int b = i & 1;
+            const int b = a.accs > 1 ? i & 1 : 0;
             const int block = 2 * w.rb + half_id;
             const int n = block * kRows + 32 * q + lane;
             float cs = 1.0f;
@@ -286,7 +303,7 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             mbar_wait_cluster(&acc_full[b], (i >> 1) & 1, aborted, status);
             tc_fence_after();
             // (after a timeout the rest runs on whatever is there: the warps keep meeting at their barriers)
-            const uint32_t acc = tmem + b * kNt + (static_cast<uint32_t>(32 * q) << 16);
+            const uint32_t acc = tmem + b * a.acc_cols + (static_cast<uint32_t>(32 * q) << 16);
             if (kSwiglu) {
                 // Gate rows are lanes 0..63 (warps q = 0, 1), their up rows lanes 64..127 (q = 2, 3).  Warps q and
                 // q ^ 2 exchange halves of 16 columns: the gate warp finishes the first 8, the up warp the others.
@@ -340,7 +357,7 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 aborted = __any_sync(0xffffffffu, aborted);
                 if (aborted) break;
                 if (mine)
-                    tma_gather4_pair(smem + ring.s * kPipeBytes + kABytes + run * 4 * kStageKBytes, &xmaps.m[0],
+                    tma_gather4_pair(smem + ring.s * a.stage_bytes + kABytes + run * 4 * kStageKBytes, &xmaps.m[0],
                                      kb * kStageK, idx, map_cluster(smem_u32(&full[ring.s]), leader));
                 __syncwarp();
             }
@@ -423,9 +440,9 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     }
     __syncwarp();
     tc_fence_before();
-    cluster_sync();   // neither CTA ends while the other's MMAs read it or its arrivals are on their way
+    cluster_sync_relaxed();   // neither CTA ends while the other's MMAs read it or its arrivals are on their way
     if (warp == 1)
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(tmem_cols) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(a.accs * a.acc_cols) : "memory");
 }
 
 // ------------------------------------------------------------------ launch
@@ -442,34 +459,41 @@ RaggedPlan wide_plan(int R, int N, int K, int E, bool int8, bool swiglu, bool ga
     // Token tiles and pairs per cluster by the estimated cycles of the longest cluster: waves x stages x a stage (its
     // bytes at 60 a cycle, or its MMAs), the last tile's columns (20 cycles each) and, if pairs share a tile, the
     // joining (2500 and 40 a column).  More, narrower tiles than `least` only for a single group, whose size the host
-    // knows.  With up to three stages, and one accumulator, two CTAs share an SM; then 33 clusters of eight CTAs or
-    // 71 of four fit the chip, else 15 or 33.
+    // knows.  Where two CTAs fit an SM, 33 clusters of eight or 71 of four run at once, else 15 or 33.
     // Measured (int8, 4096 x 7168, four pairs against one): 16 tokens 12.1 and 16.2 us; (7168 x 2048, two) 9.3 and 8.1.
     long long best = -1;
     for (int tokens = least; tokens == least || (E == 1 && tokens * pair_blocks <= kPlanSMs && tokens * 32 <= R + 31); ++tokens) {
         const int nt = tokens == least ? widest : ((R + tokens - 1) / tokens + 31) / 32 * 32;
         const int box = nt <= 32 ? 16 : (nt <= 64 ? 32 : (nt <= 128 ? 64 : 128));
-        const long long stage = kABytes + box * kStageKBytes, cycles = stage / 60 > 2 * nt ? stage / 60 : 2 * nt;
+        const int stage = kABytes + box * kStageKBytes, cycles = stage / 60 > 2 * nt ? stage / 60 : 2 * nt;
         const long long tiles = static_cast<long long>(tokens) * pair_blocks;
         for (int split = 1; split <= kMaxSplit; split *= 2) {
             const int need = split > 1 ? split * ((nt / 8 + split - 1) / split) * kRunBytes : 0;   // partial sums
-            const bool twice = need <= 3 * kPipeBytes;
+            const bool twice = need <= kHalfSmBytes;
             const int fit = split == 4 ? (twice ? 33 : 15) : (split == 2 ? (twice ? 71 : 33) : kPlanSMs / 2);
             if (split > 1 && (tiles > fit || p.kblocks < 4 * split)) continue;
             const int slice = (p.kblocks + split - 1) / split;
             const long long cost = (tiles + fit - 1) / fit * slice * cycles + 20 * nt + (split > 1 ? 2500 + 40 * nt : 0);
             if (best >= 0 && cost >= best) continue;
             best = cost;
-            const int most = split > 1 && twice ? 3 : kMaxPipe;
+            // a cluster with one tile at most: one accumulator, no more stages than it can use, and (narrow tiles) half an
+            // SM, so that the next kernel's CTAs get ready beside it
+            const bool once = tiles <= fit;
+            int stages = (once && twice && (split > 1 || nt <= 64) ? kHalfSmBytes : kMaxRingBytes) / stage;
+            if (stages > kMaxPipe) stages = kMaxPipe;
+            if (once && stages > slice) stages = slice;
             p.split = split;
-            p.nt = tokens == least ? kNt : nt;
-            p.stages = split > 1 && slice < most ? slice : most;
-            p.ring_bytes = p.stages * kPipeBytes > need ? p.stages * kPipeBytes : need;
+            p.nt = nt;
+            p.stages = stages;
+            p.stage_bytes = stage;
+            p.ring_bytes = stages * stage > need ? stages * stage : need;
             p.clusters = static_cast<int>(tiles < fit ? tiles : fit);
+            p.accs = once ? 1 : 2;
+            p.acc_cols = nt <= 32 ? 32 : (nt <= 64 ? 64 : (nt <= 128 ? 128 : 256));
         }
     }
     p.smem = 1024 + p.ring_bytes + kOffGroups + 2 * (E + 1) * 4;
-    p.threads = gather ? 32 * (kGather0 + kGatherWarps) : 256;
+    p.threads = threads_of(gather);
     return p;
 }
 
