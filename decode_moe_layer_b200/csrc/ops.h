@@ -32,18 +32,7 @@ cudaError_t launch_int8_quantize(const __nv_bfloat16 *x, bool swiglu, int8_t *q,
 cudaError_t launch_combine_rows(const void *y, bool y_f32, const float *topk_w, const int32_t *inv_pos,
                                 const __nv_bfloat16 *add, __nv_bfloat16 *out, int M, int H, int k, cudaStream_t s);
 
-// Whether a ragged product streams weight rows by warps (ragged_rows.cu) instead of tiles (ragged_wide.cu).
-constexpr int kRowsMaxTokens = 4;   // int8
-bool ragged_by_rows(int R, int E, bool int8);
-
-// How the tiles of 256 weight rows x up to nt tokens are run: `clusters` clusters of `split` CTA pairs, each pair
-// with its range of K.
-struct RaggedPlan {
-    int nt, split, clusters, stages, stage_bytes, ring_bytes, smem, threads;
-    int accs, acc_cols;        // accumulators and their columns of tensor memory
-    int row_blocks, kblocks;   // of 128 weight rows (swiglu: 64 output columns), of 128 bytes of K
-};
-RaggedPlan wide_plan(int R, int N, int K, int E, bool int8, bool swiglu, bool gather);
+struct RaggedPlan;   // ragged_plan.h
 
 struct RaggedArgs {
     const int32_t *offsets;      // [E+1]; nullptr: one group of all R rows

@@ -7,6 +7,7 @@
 
 #include "moe.h"
 #include "ops.h"
+#include "ragged_plan.h"
 
 namespace moe {
 

@@ -13,15 +13,10 @@
 
 #include "common.cuh"
 #include "ops.h"
+#include "ragged_plan.h"
 #include "tcgen05.cuh"
 
 namespace moe {
-
-namespace ragged {
-constexpr int kRows = 128;          // weight rows per CTA and tile: the lanes of tensor memory
-constexpr int kStageKBytes = 128;   // bytes of K per stage: one 128-byte swizzle row
-constexpr int kABytes = kRows * kStageKBytes;
-}  // namespace ragged
 
 // ------------------------------------------------------------------ tcgen05, both operands in shared memory
 

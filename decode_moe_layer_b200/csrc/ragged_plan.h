@@ -1,0 +1,110 @@
+// ragged_plan.h -- how the ragged products (ragged.cuh) are cut, decided on the host from the sizes alone.  No device
+// code: a host program can check it.
+#pragma once
+
+#include "moe_internal.h"
+
+namespace moe {
+
+// ------------------------------------------------------------------ by weight rows or by tiles
+
+// Measured on this part (times on the GPU, weights out of L2):
+//  * int8, 4096 x 7168: 1, 2, 4 tokens 6.4, 8.5, 9.8 us by rows against 12 by tiles; 8 tokens 11.3 against 12.1, and
+//    1536 x 2048 3.9 against 7.3, but 7168 x 2048 9.9 against 8.0.
+//  * grouped, by rows against tiles: 4 tokens x 8 of 128 experts (1536 x 2048) 33 and 40 us, 8 tokens 58 and 60,
+//    16 tokens 84 and 85, 24 tokens 108 and 101; 16 tokens x 8 of 256 experts (7168 x 2048) 418 and 438, 24 tokens
+//    592 and 585: rows of the same group begin to share a tile.
+//    With 16 rows at most the call is so short that the tiles' set-up decides: 4 tokens x 4 of 16 experts (1024 x 1024)
+//    7.2 and 8.7 us.
+constexpr int kRowsMaxTokens = 4;    // int8
+constexpr int kRowsMaxShort = 16;    // grouped
+inline bool ragged_by_rows(int R, int E, bool int8)
+{
+    if (int8) return R <= kRowsMaxTokens;
+    return 3LL * R <= 2LL * E || (R <= kRowsMaxShort && R <= E);
+}
+
+
+// ------------------------------------------------------------------ tiles (ragged_wide.cu)
+
+namespace ragged {
+constexpr int kRows = 128;          // weight rows per CTA and tile: the lanes of tensor memory
+constexpr int kStageKBytes = 128;   // bytes of K per stage: one 128-byte swizzle row
+constexpr int kABytes = kRows * kStageKBytes;
+}  // namespace ragged
+
+namespace rwide {
+using namespace ragged;
+constexpr int kMaxPipe = 8;
+constexpr int kNt = 256;                                  // most tokens per tile
+constexpr int kMaxRingBytes = 6 * (kABytes + kNt / 2 * kStageKBytes);
+constexpr int kHalfSmBytes = 102 * 1024;                  // ring of a CTA that leaves room for another on its SM
+// behind the stages
+constexpr int kOffScales = 512;                           // [2][kNt] fp32 row scales (int8)
+constexpr int kOffGroups = kOffScales + 8192;             // or, swiglu, what gate and up warps exchange: 8 KB
+static_assert(2 * kNt * 4 <= 8192 && 2 * 4 * 8 * 32 * 4 <= 8192, "either fits");
+constexpr int kEpi0 = 4, kGather0 = 8, kGatherWarps = 8;
+constexpr int threads_of(bool gather) { return 32 * (gather ? kGather0 + kGatherWarps : kGather0); }
+// split: partial sums in runs of 8 columns x 128 rows
+constexpr int kRunBytes = 8 * kRows * 4;
+constexpr int kMaxSplit = 4;                              // pairs per cluster
+}  // namespace rwide
+
+// How the tiles of 256 weight rows x up to nt tokens are run: `clusters` clusters of `split` CTA pairs, each pair
+// with its range of K.
+struct RaggedPlan {
+    int nt, split, clusters, stages, stage_bytes, ring_bytes, smem, threads;
+    int accs, acc_cols;        // accumulators and their columns of tensor memory
+    int row_blocks, kblocks;   // of 128 weight rows (swiglu: 64 output columns), of 128 bytes of K
+};
+inline RaggedPlan wide_plan(int R, int N, int K, int E, bool int8, bool swiglu, bool gather)
+{
+    using namespace rwide;
+    RaggedPlan p = {};
+    p.row_blocks = swiglu ? (N + 63) / 64 : (N + kRows - 1) / kRows;
+    p.kblocks = (K * (int8 ? 1 : 2) + kStageKBytes - 1) / kStageKBytes;
+    const int pair_blocks = (p.row_blocks + 1) / 2;
+    const int least = E == 1 ? (R + kNt - 1) / kNt : (R < E ? R : E) + R / kNt;   // token tiles of up to 256
+    const int widest = R < kNt ? (R + 31) / 32 * 32 : kNt;
+    // Token tiles and pairs per cluster by the estimated cycles of the longest cluster: waves x stages x a stage (its
+    // bytes at 60 a cycle, or its MMAs), the last tile's columns (20 cycles each) and, if pairs share a tile, the
+    // joining (2500 and 40 a column).  More, narrower tiles than `least` only for a single group, whose size the host
+    // knows.  Where two CTAs fit an SM, 33 clusters of eight or 71 of four run at once, else 15 or 33.
+    // Measured (int8, 4096 x 7168, four pairs against one): 16 tokens 12.1 and 16.2 us; (7168 x 2048, two) 9.3 and 8.1.
+    long long best = -1;
+    for (int tokens = least; tokens == least || (E == 1 && tokens * pair_blocks <= kPlanSMs && tokens * 32 <= R + 31); ++tokens) {
+        const int nt = tokens == least ? widest : ((R + tokens - 1) / tokens + 31) / 32 * 32;
+        const int box = nt <= 32 ? 16 : (nt <= 64 ? 32 : (nt <= 128 ? 64 : 128));
+        const int stage = kABytes + box * kStageKBytes, cycles = stage / 60 > 2 * nt ? stage / 60 : 2 * nt;
+        const long long tiles = static_cast<long long>(tokens) * pair_blocks;
+        for (int split = 1; split <= kMaxSplit; split *= 2) {
+            const int need = split > 1 ? split * ((nt / 8 + split - 1) / split) * kRunBytes : 0;   // partial sums
+            const bool twice = need <= kHalfSmBytes;
+            const int fit = split == 4 ? (twice ? 33 : 15) : (split == 2 ? (twice ? 71 : 33) : kPlanSMs / 2);
+            if (split > 1 && (tiles > fit || p.kblocks < 4 * split)) continue;
+            const int slice = (p.kblocks + split - 1) / split;
+            const long long cost = (tiles + fit - 1) / fit * slice * cycles + 20 * nt + (split > 1 ? 2500 + 40 * nt : 0);
+            if (best >= 0 && cost >= best) continue;
+            best = cost;
+            // a cluster with one tile at most: one accumulator, no more stages than it can use, and (narrow tiles) half an
+            // SM, so that the next kernel's CTAs get ready beside it
+            const bool once = tiles <= fit;
+            int stages = (once && twice && (split > 1 || nt <= 64) ? kHalfSmBytes : kMaxRingBytes) / stage;
+            if (stages > kMaxPipe) stages = kMaxPipe;
+            if (once && stages > slice) stages = slice;
+            p.split = split;
+            p.nt = nt;
+            p.stages = stages;
+            p.stage_bytes = stage;
+            p.ring_bytes = stages * stage > need ? stages * stage : need;
+            p.clusters = static_cast<int>(tiles < fit ? tiles : fit);
+            p.accs = once ? 1 : 2;
+            p.acc_cols = nt <= 32 ? 32 : (nt <= 64 ? 64 : (nt <= 128 ? 128 : 256));
+        }
+    }
+    p.smem = 1024 + p.ring_bytes + kOffGroups + 2 * (E + 1) * 4;
+    p.threads = threads_of(gather);
+    return p;
+}
+
+}  // namespace moe

@@ -7,7 +7,7 @@
 // one trip to memory and the stream of the weights; the tensor-core kernel's set-up costs it
 // 3 to 5 us more (int8, one token, weights out of L2: 1536 x 2048 1.9 against 7.3 us, 4096 x 7168 6.4 against 12).
 // With several groups a tile is one position of the grouped order, whose group a warp counts out of the offsets; rows
-// of the same group then read its weights from L2 again, which is why groups of more than a row or so go to the tiles (ragged_by_rows).
+// of the same group then read its weights from L2 again, which is why groups of more than a row or so go to the tiles (ragged_by_rows, ragged_plan.h).
 // The order of the sums is fixed: lane, then the reduction tree.
 #include "ragged.cuh"
 
@@ -170,14 +170,6 @@ ragged_rows_kernel(const void *wbase, const __grid_constant__ RaggedArgs a, int 
 }
 
 // ------------------------------------------------------------------ launch
-
-// Measured on this part (times on the GPU, weights out of L2):
-//  * int8, 4096 x 7168: 1, 2, 4 tokens 6.4, 8.5, 9.8 us by rows against 12 by tiles; 8 tokens 11.3 against 12.1, and
-//    1536 x 2048 3.9 against 7.3, but 7168 x 2048 9.9 against 8.0.
-//  * grouped, by rows against tiles: 4 tokens x 8 of 128 experts (1536 x 2048) 33 and 40 us, 8 tokens 58 and 60,
-//    16 tokens 84 and 85, 24 tokens 108 and 101; 16 tokens x 8 of 256 experts (7168 x 2048) 418 and 438, 24 tokens
-//    592 and 585: rows of the same group begin to share a tile.
-bool ragged_by_rows(int R, int E, bool int8) { return int8 ? R <= kRowsMaxTokens : 3LL * R <= 2LL * E; }
 
 template <bool kInt8, bool kSwiglu, int kT>
 static cudaError_t launch_rows_t(const void *w, const RaggedArgs &a, cudaStream_t s)

@@ -30,25 +30,9 @@
 #include <atomic>
 
 #include "ragged.cuh"
+#include "ragged_plan.h"
 
 namespace moe {
-
-namespace rwide {
-using namespace ragged;
-constexpr int kMaxPipe = 8;
-constexpr int kNt = 256;                                  // most tokens per tile
-constexpr int kMaxRingBytes = 6 * (kABytes + kNt / 2 * kStageKBytes);
-constexpr int kHalfSmBytes = 102 * 1024;                  // ring of a CTA that leaves room for another on its SM
-// behind the stages
-constexpr int kOffScales = 512;                           // [2][kNt] fp32 row scales (int8)
-constexpr int kOffGroups = kOffScales + 8192;             // or, swiglu, what gate and up warps exchange: 8 KB
-static_assert(2 * kNt * 4 <= 8192 && 2 * 4 * 8 * 32 * 4 <= 8192, "either fits");
-constexpr int kEpi0 = 4, kGather0 = 8, kGatherWarps = 8;
-constexpr int threads_of(bool gather) { return 32 * (gather ? kGather0 + kGatherWarps : kGather0); }
-// split: partial sums in runs of 8 columns x 128 rows
-constexpr int kRunBytes = 8 * kRows * 4;
-constexpr int kMaxSplit = 4;                              // pairs per cluster
-}  // namespace rwide
 
 // Copies that complete on a barrier of either CTA of the pair (bar: cluster address).
 __device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map, int c0, int c1, uint32_t bar)
@@ -236,6 +220,13 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             }
             if (aborted) break;
         }
+        // the MMA warp's releases of the last stages arrive while this CTA lives
+        if (issued >= a.stages) {
+            for (int i = 0; i < a.stages; ++i, ring.next())
+                mbar_wait(&empty[ring.s], ring.parity ^ 1, aborted, status);
+        } else {
+            for (int i = 0; i < issued; ++i) mbar_wait(&empty[i], 0, aborted, status);
+        }
         // after a timeout the even CTA waits for both CTAs' copies in flight: the stages before the one it gave up on
         if (aborted && half_id == 0)
             for (int i = 0; i < a.stages && i < issued; ++i) {
@@ -261,7 +252,8 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     } else if (warp == 1 && half_id == 0) {
         // ------------------------------------------------------------ MMA issuer
         Ring ring(a.stages);
-        for (int i = 0; w.locate(); w.next(), ++i) {
+        int i = 0;
+        for (; w.locate(); w.next(), ++i) {
             const int b = a.accs > 1 ? i & 1 : 0, n32 = (w.count + 31) & ~31;
             const uint32_t idesc = kInt8 ? umma_idesc_i8(256, n32) : umma_idesc_bf16(256, n32);
             const uint32_t acc = tmem + b * a.acc_cols;
@@ -285,6 +277,10 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             if (elect_one()) umma_commit_pair(smem_u32(&acc_full[b]), leader);
             __syncwarp();
         }
+        // the epilogues' last arrivals, of the other CTA too, land while this CTA lives
+        if (split == 1)
+            for (int j = i > 1 ? i - 2 : 0; j < i; ++j)
+                mbar_wait_cluster(&acc_empty[a.accs > 1 ? j & 1 : 0], (j >> 1) & 1, aborted, status);
     } else if (warp >= kEpi0 && warp < kEpi0 + 4 && split == 1) {
         // ------------------------------------------------------------ epilogue
         const int q = warp - kEpi0;
@@ -440,62 +436,17 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     }
     __syncwarp();
     tc_fence_before();
-    cluster_sync_relaxed();   // neither CTA ends while the other's MMAs read it or its arrivals are on their way
+    // Neither CTA ends while the other's MMAs read it.  What a CTA sent to another has been waited for there, so nothing
+    // needs ordering; a warp that gave up on a wait cannot know, and orders everything.
+    if (aborted)
+        cluster_sync();
+    else
+        cluster_sync_relaxed();
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(a.accs * a.acc_cols) : "memory");
 }
 
 // ------------------------------------------------------------------ launch
-
-RaggedPlan wide_plan(int R, int N, int K, int E, bool int8, bool swiglu, bool gather)
-{
-    using namespace rwide;
-    RaggedPlan p = {};
-    p.row_blocks = swiglu ? (N + 63) / 64 : (N + kRows - 1) / kRows;
-    p.kblocks = (K * (int8 ? 1 : 2) + kStageKBytes - 1) / kStageKBytes;
-    const int pair_blocks = (p.row_blocks + 1) / 2;
-    const int least = E == 1 ? (R + kNt - 1) / kNt : (R < E ? R : E) + R / kNt;   // token tiles of up to 256
-    const int widest = R < kNt ? (R + 31) / 32 * 32 : kNt;
-    // Token tiles and pairs per cluster by the estimated cycles of the longest cluster: waves x stages x a stage (its
-    // bytes at 60 a cycle, or its MMAs), the last tile's columns (20 cycles each) and, if pairs share a tile, the
-    // joining (2500 and 40 a column).  More, narrower tiles than `least` only for a single group, whose size the host
-    // knows.  Where two CTAs fit an SM, 33 clusters of eight or 71 of four run at once, else 15 or 33.
-    // Measured (int8, 4096 x 7168, four pairs against one): 16 tokens 12.1 and 16.2 us; (7168 x 2048, two) 9.3 and 8.1.
-    long long best = -1;
-    for (int tokens = least; tokens == least || (E == 1 && tokens * pair_blocks <= kPlanSMs && tokens * 32 <= R + 31); ++tokens) {
-        const int nt = tokens == least ? widest : ((R + tokens - 1) / tokens + 31) / 32 * 32;
-        const int box = nt <= 32 ? 16 : (nt <= 64 ? 32 : (nt <= 128 ? 64 : 128));
-        const int stage = kABytes + box * kStageKBytes, cycles = stage / 60 > 2 * nt ? stage / 60 : 2 * nt;
-        const long long tiles = static_cast<long long>(tokens) * pair_blocks;
-        for (int split = 1; split <= kMaxSplit; split *= 2) {
-            const int need = split > 1 ? split * ((nt / 8 + split - 1) / split) * kRunBytes : 0;   // partial sums
-            const bool twice = need <= kHalfSmBytes;
-            const int fit = split == 4 ? (twice ? 33 : 15) : (split == 2 ? (twice ? 71 : 33) : kPlanSMs / 2);
-            if (split > 1 && (tiles > fit || p.kblocks < 4 * split)) continue;
-            const int slice = (p.kblocks + split - 1) / split;
-            const long long cost = (tiles + fit - 1) / fit * slice * cycles + 20 * nt + (split > 1 ? 2500 + 40 * nt : 0);
-            if (best >= 0 && cost >= best) continue;
-            best = cost;
-            // a cluster with one tile at most: one accumulator, no more stages than it can use, and (narrow tiles) half an
-            // SM, so that the next kernel's CTAs get ready beside it
-            const bool once = tiles <= fit;
-            int stages = (once && twice && (split > 1 || nt <= 64) ? kHalfSmBytes : kMaxRingBytes) / stage;
-            if (stages > kMaxPipe) stages = kMaxPipe;
-            if (once && stages > slice) stages = slice;
-            p.split = split;
-            p.nt = nt;
-            p.stages = stages;
-            p.stage_bytes = stage;
-            p.ring_bytes = stages * stage > need ? stages * stage : need;
-            p.clusters = static_cast<int>(tiles < fit ? tiles : fit);
-            p.accs = once ? 1 : 2;
-            p.acc_cols = nt <= 32 ? 32 : (nt <= 64 ? 64 : (nt <= 128 ? 128 : 256));
-        }
-    }
-    p.smem = 1024 + p.ring_bytes + kOffGroups + 2 * (E + 1) * 4;
-    p.threads = threads_of(gather);
-    return p;
-}
 
 template <bool kInt8, bool kGather, bool kSwiglu>
 static cudaError_t launch_wide_t(const CUtensorMap &wmap, const BoxMaps &xmaps, const RaggedArgs &a,

@@ -170,7 +170,7 @@ def int8_ref(q, qs, w, ws):
 INT8_SHAPES = [(1, 8, 16), (1, 1, 16), (1, 4096, 7168), (2, 1000, 528), (16, 128, 128), (17, 129, 144), (31, 512, 2048),
                (33, 1536, 2048), (64, 256, 4096), (65, 200, 1040), (100, 640, 512), (129, 96, 256), (200, 1024, 768),
                (256, 128, 1024), (257, 384, 2048), (513, 2056, 400), (1000, 4096, 1536),
-               (2100, 2700, 272), (1500, 4100, 2000), (5000, 1000, 1024)]
+               (40, 1000, 8192), (100, 4096, 7168), (200, 1500, 4112), (6, 200, 65536), (2100, 2700, 272), (1500, 4100, 2000), (5000, 1000, 1024)]
 
 
 @pytest.mark.parametrize("M,N,K", INT8_SHAPES)
@@ -257,7 +257,8 @@ GROUPED_SHAPES = [
     (129, 8, 8, 160, 136, "skew"), (700, 8, 16, 512, 1024, "uniform"), (1024, 8, 128, 256, 1536, "skew"),
     (513, 4, 2, 1024, 2048, "skew"), (1500, 2, 3, 1296, 200, "skew"), (700, 8, 32, 1536, 520, "uniform"),
     (640, 8, 100, 1024, 1024, "skew"), (5000, 1, 1, 528, 1032, "uniform"),
-    (33, 2, 5, 77, 64, "uniform"), (5, 3, 7, 1001, 1000, "skew"), (2000, 1, 2, 2051, 136, "skew"),
+    (40, 2, 3, 520, 4096, "skew"), (300, 1, 2, 130, 8192, "skew"), (20, 1, 1, 1000, 4104, "uniform"),
+    (600, 2, 2, 200, 4096, "skew"), (33, 2, 5, 77, 64, "uniform"), (5, 3, 7, 1001, 1000, "skew"), (2000, 1, 2, 2051, 136, "skew"),
 ]
 
 

@@ -1,12 +1,17 @@
 """Argument checks of the operators around the routed layer: the C entry points refuse before they make any CUDA
 call, and the Python binding refuses tensors of the wrong type, shape, layout or device.  No GPU."""
 import ctypes
+import os
+import shutil
+import subprocess
 
 import pytest
 import torch
 
 import decode_moe_layer_b200 as moe
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 P = ctypes.c_void_p
 INV, UNS, OK = moe.MOE_ERR_INVALID_ARG, moe.MOE_ERR_UNSUPPORTED_SHAPE, moe.MOE_OK
 
@@ -105,3 +110,15 @@ def test_binding_refuses_cpu_tensors_and_wrong_types():
                  lambda: moe.moe_combine(x, x[:, :1].float(), torch.zeros(2, dtype=torch.int32))):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.skipif(not os.path.exists(NVCC) and shutil.which("nvcc") is None, reason="needs nvcc")
+def test_ragged_plans_hold_over_a_grid_of_shapes(tmp_path):
+    exe = str(tmp_path / "ragged_plan_check")
+    subprocess.check_call([NVCC if os.path.exists(NVCC) else shutil.which("nvcc"), "-gencode",
+                           "arch=compute_100a,code=sm_100a", "-std=c++17", "-O1", "--expt-relaxed-constexpr",
+                           "-I", os.path.join(ROOT, "decode_moe_layer_b200", "csrc"),
+                           "-I", os.path.join(ROOT, "include"),
+                           os.path.join(ROOT, "tests", "host", "ragged_plan_check.cu"), "-o", exe])
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.startswith("ok"), r.stdout + r.stderr
