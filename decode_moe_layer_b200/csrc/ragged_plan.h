@@ -64,7 +64,7 @@ inline RaggedPlan wide_plan(int R, int N, int K, int E, bool int8, bool swiglu, 
     p.row_blocks = swiglu ? (N + 63) / 64 : (N + kRows - 1) / kRows;
     p.kblocks = (K * (int8 ? 1 : 2) + kStageKBytes - 1) / kStageKBytes;
     const int pair_blocks = (p.row_blocks + 1) / 2;
-    const int least = E == 1 ? (R + kNt - 1) / kNt : (R < E ? R : E) + R / kNt;   // token tiles of up to 256
+    const int least = E == 1 ? (R + kNt - 1) / kNt : (R < E ? R : E) + (R - 1) / kNt;   // token tiles of up to 256
     const int widest = R < kNt ? (R + 31) / 32 * 32 : kNt;
     // Token tiles and pairs per cluster by the estimated cycles of the longest cluster: waves x stages x a stage (its
     // bytes at 60 a cycle, or its MMAs), the last tile's columns (20 cycles each) and, if pairs share a tile, the

@@ -40,8 +40,7 @@ int main()
                         // several groups: only the widest tile is sure to cut each as counted
                         CHECK(E == 1 || p.nt == 256 || p.nt >= R);
                         // token tiles at most: one per group that has rows, and one more for each nt rows above it
-                        const long long tokens =
-                            E == 1 ? (R + p.nt - 1) / p.nt : (R < E ? R : E) + (p.nt >= R ? 0 : R / p.nt);
+                        const long long tokens = E == 1 ? (R + p.nt - 1) / p.nt : (R < E ? R : E) + (R - 1) / p.nt;
                         const long long tiles = tokens * ((p.row_blocks + 1) / 2);
                         CHECK(tiles < (1LL << 31));
                         CHECK(p.clusters >= 1 && p.clusters <= tiles && 2 * p.split * p.clusters <= 2 * kPlanSMs);
