@@ -38,6 +38,7 @@ using namespace ragged;
 constexpr int kMaxPipe = 8;
 constexpr int kNt = 256;                                  // most tokens per tile
 constexpr int kMaxRingBytes = 6 * (kABytes + kNt / 2 * kStageKBytes);
+constexpr int kSmBytes = 228 * 1024, kReservedBytes = 1024;   // shared memory of an SM; what a CTA takes besides its own
 constexpr int kHalfSmBytes = 102 * 1024;                  // ring of a CTA that leaves room for another on its SM
 // behind the stages
 constexpr int kOffScales = 512;                           // [2][kNt] fp32 row scales (int8)
@@ -103,6 +104,11 @@ inline RaggedPlan wide_plan(int R, int N, int K, int E, bool int8, bool swiglu, 
         }
     }
     p.smem = 1024 + p.ring_bytes + kOffGroups + 2 * (E + 1) * 4;
+    // An SM's CTAs, of whatever calls, must not ask for more tensor memory than there is: a CTA that waits for some while
+    // its pair holds some could wait on one that waits on it.  So a CTA takes at least its columns' share of an SM's
+    // shared memory.
+    const int share = p.accs * p.acc_cols * (kSmBytes / 512) - kReservedBytes;
+    if (p.smem < share) p.smem = share;
     p.threads = threads_of(gather);
     return p;
 }

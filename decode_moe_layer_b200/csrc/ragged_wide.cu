@@ -58,9 +58,12 @@ __device__ __forceinline__ void umma_commit_pair(uint32_t mbar_smem, uint32_t le
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
                  ::"r"(mbar_smem), "h"(static_cast<uint16_t>(3u << leader)) : "memory");
 }
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr)
+// Arrival of an epilogue warp that is done with an accumulator.  Its loads from tensor memory have completed
+// (tcgen05.wait::ld), and there is no other memory to order; the releasing form would wait until the warp's stores to
+// y have arrived, some 1300 cycles a tile.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity)
 {
@@ -330,7 +333,7 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_cluster(smem_u32(&acc_empty[b]), leader));
+            if (lane == 0) mbar_arrive_cluster_relaxed(map_cluster(smem_u32(&acc_empty[b]), leader));
         }
     } else if (kGather && warp >= kGather0) {
         // ------------------------------------------------------------ gather

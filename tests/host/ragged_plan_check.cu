@@ -34,9 +34,10 @@ int main()
                         // a stage holds the box of half a tile
                         const int half = p.nt / 2, box = half <= 16 ? 16 : (half <= 32 ? 32 : (half <= 64 ? 64 : 128));
                         CHECK(p.stage_bytes == rwide::kABytes + box * rwide::kStageKBytes);
-                        // tensor memory: a power of two of columns, two such CTAs on an SM where two fit it
-                        CHECK(p.acc_cols >= p.nt && (p.acc_cols & (p.acc_cols - 1)) == 0 && p.accs * p.acc_cols <= 512);
-                        CHECK(2 * (p.smem + 1024) > 228 * 1024 || p.accs * p.acc_cols <= 256);
+                        // tensor memory: a power of two of columns, and no more of it than of shared memory
+                        const long long cols = static_cast<long long>(p.accs) * p.acc_cols;
+                        CHECK(p.acc_cols >= p.nt && (p.acc_cols & (p.acc_cols - 1)) == 0 && cols <= 512);
+                        CHECK((p.smem + 1024LL) * 512 >= cols * 228 * 1024);
                         // several groups: only the widest tile is sure to cut each as counted
                         CHECK(E == 1 || p.nt == 256 || p.nt >= R);
                         // token tiles at most: one per group that has rows, and one more for each nt rows above it

@@ -68,7 +68,7 @@ def norm_ref(x, residual, w_post, gate, w_pre, eps, rs, bs, off):
 
 
 @pytest.mark.parametrize("M,H", [(1, 8), (1, 7168), (3, 264), (5, 1000), (33, 2048), (2, 8192), (2, 8200), (7, 16384),
-                                 (700, 512)])
+                                 (700, 512), (600, 4104), (593, 16384), (1500, 1024)])
 @pytest.mark.parametrize("gate", ["none", "channel", "token", "full"])
 @pytest.mark.parametrize("post,res,pre", [(True, True, True), (False, True, True), (True, False, True),
                                           (True, True, False), (False, False, True)])
@@ -114,6 +114,15 @@ def test_block_norm_in_place_and_plain(moe):
     y = torch.empty_like(x)
     n, h2 = moe.moe_block_norm(x, w_pre=w, res_out=y)
     assert torch.equal(y, x) and torch.equal(h, h2)
+
+
+def test_block_norm_token_gate_as_column(moe):
+    g = gen(8)
+    x, r, w = randn(g, 9, 640), randn(g, 9, 640), randn(g, 640)
+    t = torch.rand(9, generator=g, device="cuda")
+    a = moe.moe_block_norm(x, residual=r, gate=t, w_pre=w)
+    b = moe.moe_block_norm(x, residual=r, gate=t[:, None].contiguous(), w_pre=w)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
 def test_block_norm_zero_rows_and_nan_rows(moe):
@@ -554,3 +563,34 @@ def test_binding_refusals(moe):
         moe.moe_grouped_gemm(x, randn(g, 2, 16, 64), torch.zeros(2, dtype=torch.int32, device="cuda"))
     with pytest.raises(ValueError):
         moe.moe_combine(x, torch.ones(2, 3, device="cuda"), torch.zeros(6, dtype=torch.int32, device="cuda"))
+    z = torch.zeros(3, dtype=torch.int32, device="cuda")
+    w3 = randn(g, 2, 16, 64)
+    with pytest.raises(ValueError):
+        moe.moe_grouped_gemm(x, w3.transpose(1, 2).contiguous().transpose(1, 2), z)
+    with pytest.raises(ValueError):
+        moe.moe_grouped_gemm(x, w3, z.long())
+    with pytest.raises(ValueError):
+        moe.moe_grouped_gemm(x, w3, z, torch.zeros(9, dtype=torch.int32, device="cuda"), k=2)
+    with pytest.raises(ValueError):
+        moe.moe_grouped_gemm(x, w3, z, torch.zeros(0, dtype=torch.int32, device="cuda"), k=0)
+    with pytest.raises(ValueError):
+        moe.moe_grouped_gemm(x, w3[:, :15].contiguous(), z, swiglu=True)
+    with pytest.raises(ValueError):
+        moe.moe_grouped_gemm(x, w3, z, out=torch.zeros(4, 16, device="cuda"))
+    with pytest.raises(ValueError):
+        moe.moe_grouped_gemm(x, w3, z, out_dtype=torch.float16)
+    with pytest.raises(moe.MoEError):
+        moe.moe_grouped_gemm(randn(g, 4, 20), randn(g, 2, 16, 20), z)
+    with pytest.raises(TypeError):
+        moe.moe_grouped_gemm(x, w3, None)
+    with pytest.raises(ValueError):
+        moe.moe_int8_gemm(*moe.moe_int8_quantize(x), torch.zeros(8, 32, dtype=torch.int8, device="cuda"), w[:8].float())
+    with pytest.raises(ValueError):
+        moe.moe_int8_quantize(x, stream=_FakeStream(torch.device("cuda", 1)))
+    assert moe.moe_combine(x[:0], torch.ones(0, 3, device="cuda"), z[:0]).shape == (0, 64)
+    assert moe.moe_block_norm(x[:0], w_pre=w)[1].shape == (0, 64)
+
+
+class _FakeStream:
+    def __init__(self, device):
+        self.device = device
