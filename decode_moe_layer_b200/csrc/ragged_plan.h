@@ -8,14 +8,14 @@ namespace moe {
 
 // ------------------------------------------------------------------ by weight rows or by tiles
 
-// Measured on this part (times on the GPU, weights out of L2):
-//  * int8, 4096 x 7168: 1, 2, 4 tokens 6.4, 8.5, 9.8 us by rows against 12 by tiles; 8 tokens 11.3 against 12.1, and
-//    1536 x 2048 3.9 against 7.3, but 7168 x 2048 9.9 against 8.0.
-//  * grouped, by rows against tiles: 4 tokens x 8 of 128 experts (1536 x 2048) 33 and 40 us, 8 tokens 58 and 60,
-//    16 tokens 84 and 85, 24 tokens 108 and 101; 16 tokens x 8 of 256 experts (7168 x 2048) 418 and 438, 24 tokens
-//    592 and 585: rows of the same group begin to share a tile.
-//    With 16 rows at most the call is so short that the tiles' set-up decides: 4 tokens x 4 of 16 experts (1024 x 1024)
-//    7.2 and 8.7 us.
+// Measured on this part (times on the GPU, weights out of L2), by rows against tiles:
+//  * int8: 4096 x 7168 with 1, 2, 4 tokens 6.4, 8.5, 9.7 us against 9.8, with 8 tokens 11.3; 1536 x 2048 with 1, 2, 4
+//    tokens 1.9, 2.8, 3.6 us against 5.9; 7168 x 2048 with 4 tokens 6.1 against 7.1, with 8 9.9.
+//  * grouped, 128 experts of 1536 x 2048, top-8: 4, 8, 12, 16 tokens 29, 52, 69, 84 us against 37, 56, 68, 79; 256
+//    experts of 7168 x 2048: 8, 16, 20, 32 tokens 235, 414, 495, 727 us against 237, 416, 505, 681.  From about 0.7
+//    rows a group on, groups of two and more rows pay for a tile.
+//  * with 16 rows at most the call is so short that the tiles' set-up decides: 4 tokens x 4 of 16 experts of 1024 x 1024
+//    6.2 us against 8.5.
 constexpr int kRowsMaxTokens = 4;    // int8
 constexpr int kRowsMaxShort = 16;    // grouped
 inline bool ragged_by_rows(int R, int E, bool int8)
@@ -71,7 +71,8 @@ inline RaggedPlan wide_plan(int R, int N, int K, int E, bool int8, bool swiglu, 
     // bytes at 60 a cycle, or its MMAs), the last tile's columns (20 cycles each) and, if pairs share a tile, the
     // joining (2500 and 40 a column).  More, narrower tiles than `least` only for a single group, whose size the host
     // knows.  Where two CTAs fit an SM, 33 clusters of eight or 71 of four run at once, else 15 or 33.
-    // Measured (int8, 4096 x 7168, four pairs against one): 16 tokens 12.1 and 16.2 us; (7168 x 2048, two) 9.3 and 8.1.
+    // Measured (int8, 4096 x 7168): 16 tokens by four pairs a tile 9.8 us, by one 16; 256 tokens as four tiles of 64 by two
+    // pairs 15, as one by four 20, as one by one 23.
     long long best = -1;
     for (int tokens = least; tokens == least || (E == 1 && tokens * pair_blocks <= kPlanSMs && tokens * 32 <= R + 31); ++tokens) {
         const int nt = tokens == least ? widest : ((R + tokens - 1) / tokens + 31) / 32 * 32;

@@ -4,8 +4,9 @@
 // kW rows at a time (swiglu: a gate row and its up row), the next 16 to 32 loads of a lane always on their way while
 // it works on the last; products and sums on the ordinary pipes (fp32 FMA; dp4a into int32), a warp reduction at the
 // end of a row.  No tensor map, barrier, cluster or tensor memory: what a call of this size waits for is the launch,
-// one trip to memory and the stream of the weights; the tensor-core kernel's set-up costs it
-// 3 to 5 us more (int8, one token, weights out of L2: 1536 x 2048 1.9 against 7.3 us, 4096 x 7168 6.4 against 12).
+// one trip to memory and the stream of the weights; the tensor-core kernel's set-up costs it 3 to 4 us more (int8, one
+// token, weights out of L2: 1536 x 2048 1.9 against 5.9 us, 4096 x 7168 6.4 against 9.8; the weights alone 0.5 and
+// 4.5).  8 of 128 experts of 1536 x 2048 with a row each: 10.4 us, 50 MB.
 // With several groups a tile is one position of the grouped order, whose group a warp counts out of the offsets; rows
 // of the same group then read its weights from L2 again, which is why groups of more than a row or so go to the tiles (ragged_by_rows, ragged_plan.h).
 // The order of the sums is fixed: lane, then the reduction tree.
@@ -18,7 +19,7 @@ constexpr int kWarps = 4;
 // rows at a time and 512-byte runs of each in flight: tokens share the weights' registers
 constexpr int rows_of(bool int8, int t) { return int8 && t > 1 ? 4 : 2; }
 constexpr int runs_of(bool int8, int t) { return int8 && t > 1 ? 2 : 4; }
-constexpr int kWarpsPerSm = 16;   // aimed at
+constexpr int kWarpsPerSm = 64;   // aimed at: more than an SM holds, so that SMs that are done early find work
 }  // namespace rrows
 
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
