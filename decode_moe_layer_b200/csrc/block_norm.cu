@@ -49,21 +49,40 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8])
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The code of v for the row scale s = max / 127: rne(v / s), |code| <= 127; a row of zeros has s = 0 and codes 0.
-__device__ __forceinline__ uint32_t int8_code(float v, float s)
+// The codes rne(v / s) of eight values for the row scale s = max / 127, |code| <= 127; a row of zeros has s = 0 and
+// codes 0.  `inv` is 1 / s.  v * inv is off from the rounded quotient by less than 127 * 2^-22, so the two round to the
+// same integer unless it lies that near to a half: only then (one value in ten thousand) are the quotients taken.
+// Rounded with a division each, the codes took 2.5 times as long as their memory traffic.  Rows so small that 1 / s
+// overflows divide as well.
+struct CodeScale {
+    float s, inv;
+    __device__ __forceinline__ explicit CodeScale(float max_abs) : s(max_abs / 127.0f), inv(0.f)
+    {
+        if (s > 0x1p-120f) inv = 1.0f / s;
+    }
+};
+__device__ __forceinline__ uint32_t int8_code_exact(float v, float s)
 {
     const int c = s > 0.f ? __float2int_rn(v / s) : 0;
-    return static_cast<uint32_t>(max(-127, min(127, c))) & 0xFFu;
+    return static_cast<uint32_t>(max(-127, min(127, c)));
 }
-__device__ __forceinline__ uint2 int8_codes8(const float (&f)[8], float s)
+__device__ __forceinline__ uint2 int8_codes8(const float (&f)[8], const CodeScale &k)
 {
-    uint32_t lo = 0, hi = 0;
+    constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23: adding it rounds to an integer, held in the low bits
+    uint32_t c[8];
+    float far = 0.f;                        // largest distance from the integer taken
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        lo |= int8_code(f[i], s) << (8 * i);
-        hi |= int8_code(f[4 + i], s) << (8 * i);
+    for (int i = 0; i < 8; ++i) {
+        const float t = f[i] * k.inv, m = t + kMagic;
+        c[i] = __float_as_uint(m);
+        far = fmaxf(far, fabsf(t - (m - kMagic)));
     }
-    return make_uint2(lo, hi);
+    if (!(far < 0.4999f) || k.inv == 0.f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = int8_code_exact(f[i], k.s);
+    }
+    return make_uint2(prmt(prmt(c[0], c[1], 0x0040u), prmt(c[2], c[3], 0x0040u), 0x5410u),
+                      prmt(prmt(c[4], c[5], 0x0040u), prmt(c[6], c[7], 0x0040u), 0x5410u));
 }
 
 // Sum and maximum of a pair over the CTA; every thread gets both.  `buf` holds one pair per warp and is
@@ -165,8 +184,8 @@ __global__ void __launch_bounds__(norm::kMaxThreads) block_norm_kernel(const __g
     if (a.w_pre == nullptr) return;
     const float2 st = block_sum_max(ss2, mx, red[1]);
     const float inv = rsqrtf(st.x * inv_h + a.eps);
-    const float qs = st.y * inv / 127.0f;
-    if (a.q_out != nullptr && threadIdx.x == 0) a.q_s[row] = qs;
+    const CodeScale qs(st.y * inv);
+    if (a.q_out != nullptr && threadIdx.x == 0) a.q_s[row] = qs.s;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = threadIdx.x + i * blockDim.x;
@@ -353,8 +372,8 @@ block_norm_ring_kernel(const __grid_constant__ NormArgs a, int stages)
             const float2 sum = block_sum_max(ss.x + ss.y, mx, red[1]);
             const float inv = rsqrtf(sum.x * inv_h + a.eps);
             const f2 inv2 = {inv, inv};
-            const float qs = sum.y * inv / 127.0f;
-            if (kQuant && threadIdx.x == 0) a.q_s[row] = qs;
+            const CodeScale qs(sum.y * inv);
+            if (kQuant && threadIdx.x == 0) a.q_s[row] = qs.s;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int c = threadIdx.x + i * blockDim.x;
@@ -379,46 +398,54 @@ block_norm_ring_kernel(const __grid_constant__ NormArgs a, int stages)
     }
 }
 
+// silu(min(g, 7)) * clamp(u, -7, 7) for the codes: exp and the division by their fast forms, off by less than 2^-16
+// of the value for |g| <= 80, against a code's step of 2^-8 of the row's largest.
+__device__ __forceinline__ float swiglu_fast(float g, float u)
+{
+    const float a = fminf(g, 7.0f);
+    return __fdividef(a, 1.0f + __expf(-a)) * fminf(fmaxf(u, -7.0f), 7.0f);
+}
+
 // Codes of the rows of x [M, K], or of clamp-SwiGLU of the rows' halves [gate | up] ([M, 2K], kSwiglu;
-// the activation stays in fp32).
+// the activation stays in fp32).  A CTA per row with V vectors a thread: all loads of a row go out at once, and the
+// other CTAs of the SM load while this one reduces.
 template <int V, bool kSwiglu>
-__global__ void __launch_bounds__(norm::kMaxThreads)
-int8_quantize_kernel(const __nv_bfloat16 *x, int8_t *q, float *q_s, int M, int K)
+__global__ void __launch_bounds__(V == 1 ? norm::kMaxThreads : norm::kMaxThreads / 2)
+int8_quantize_kernel(const __nv_bfloat16 *x, int8_t *q, float *q_s, int K)
 {
     using norm::kVec;
-    __shared__ float2 red[2][32];
-    const int nvec = K / kVec;
+    __shared__ float2 red[32];
+    const int nvec = K / kVec, row = blockIdx.x;
+    const uint4 *src = reinterpret_cast<const uint4 *>(x) + static_cast<size_t>(row) * nvec * (kSwiglu ? 2 : 1);
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
     pdl_wait();
     pdl_trigger();
-    int turn = 0;
-    for (int row = blockIdx.x; row < M; row += gridDim.x, turn ^= 1) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(x) + static_cast<size_t>(row) * nvec * (kSwiglu ? 2 : 1);
-        float v[V][8];
-        float mx = 0.f;
+    uint4 p[V][kSwiglu ? 2 : 1];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = threadIdx.x + i * blockDim.x;
-            if (c >= nvec) continue;
-            unpack8(src[c], v[i]);
-            if (kSwiglu) {
-                float u[8];
-                unpack8(src[nvec + c], u);
+    for (int i = 0; i < V; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        p[i][0] = c < nvec ? src[c] : zero;
+        if (kSwiglu) p[i][kSwiglu ? 1 : 0] = c < nvec ? src[nvec + c] : zero;
+    }
+    float v[V][8], mx = 0.f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float g = fminf(v[i][j], 7.0f);
-                    v[i][j] = g / (1.0f + expf(-g)) * fminf(fmaxf(u[j], -7.0f), 7.0f);
-                }
-            }
+    for (int i = 0; i < V; ++i) {
+        unpack8(p[i][0], v[i]);
+        if (kSwiglu) {
+            float u[8];
+            unpack8(p[i][kSwiglu ? 1 : 0], u);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(v[i][j]));
+            for (int j = 0; j < 8; ++j) v[i][j] = swiglu_fast(v[i][j], u[j]);
         }
-        const float s = block_sum_max(0.f, mx, red[turn]).y / 127.0f;
-        if (threadIdx.x == 0) q_s[row] = s;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = threadIdx.x + i * blockDim.x;
-            if (c < nvec) reinterpret_cast<uint2 *>(q)[static_cast<size_t>(row) * nvec + c] = int8_codes8(v[i], s);
-        }
+        for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(v[i][j]));
+    }
+    const CodeScale s(block_sum_max(0.f, mx, red).y);
+    if (threadIdx.x == 0) q_s[row] = s.s;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        if (c < nvec) reinterpret_cast<uint2 *>(q)[static_cast<size_t>(row) * nvec + c] = int8_codes8(v[i], s);
     }
 }
 
@@ -483,13 +510,14 @@ cudaError_t launch_int8_quantize(const __nv_bfloat16 *x, bool swiglu, int8_t *q,
                                  cudaStream_t s)
 {
     const int nvec = K / norm::kVec;
-    const int v = nvec <= norm::kMaxThreads ? 1 : 2;
+    // a vector a thread for few rows, which wait for one trip to memory; four for many
+    const int v = M <= kPlanSMs && nvec <= norm::kMaxThreads ? 1 : 4;
     const dim3 threads(row_threads(nvec, v)), grid(M);
     if (swiglu)
-        return v == 1 ? launch_ex(int8_quantize_kernel<1, true>, grid, threads, 0, s, true, x, q, q_s, M, K)
-                      : launch_ex(int8_quantize_kernel<2, true>, grid, threads, 0, s, true, x, q, q_s, M, K);
-    return v == 1 ? launch_ex(int8_quantize_kernel<1, false>, grid, threads, 0, s, true, x, q, q_s, M, K)
-                  : launch_ex(int8_quantize_kernel<2, false>, grid, threads, 0, s, true, x, q, q_s, M, K);
+        return v == 1 ? launch_ex(int8_quantize_kernel<1, true>, grid, threads, 0, s, true, x, q, q_s, K)
+                      : launch_ex(int8_quantize_kernel<4, true>, grid, threads, 0, s, true, x, q, q_s, K);
+    return v == 1 ? launch_ex(int8_quantize_kernel<1, false>, grid, threads, 0, s, true, x, q, q_s, K)
+                  : launch_ex(int8_quantize_kernel<4, false>, grid, threads, 0, s, true, x, q, q_s, K);
 }
 
 }  // namespace moe
