@@ -51,12 +51,14 @@ static int run_ragged(bool int8, bool swiglu, const void *w, uint64_t w_rows, Ra
     a.kblocks = p.kblocks;
     a.split = p.split;
     a.ring_bytes = p.ring_bytes;
-    // weight boxes of 128 rows, or (swiglu) of 64 gate rows and of 64 up rows; token boxes of every height
+    // weight boxes of 128 rows, or (swiglu) of 64 gate rows and of 64 up rows; token boxes of the heights that tiles
+    // can have
     CUtensorMap wmap;
     BoxMaps maps;
     const uint64_t rows = static_cast<uint64_t>(a.M), K = static_cast<uint64_t>(a.K);
     int rc = encode_rows_map(&wmap, int8, w, w_rows, K, swiglu ? 64 : 128);
-    for (int i = 0; i < (gather ? 1 : 4) && rc == MOE_OK; ++i)
+    const int top = gather ? 0 : rwide::box_of(p.nt / 2);
+    for (int i = a.offsets != nullptr ? 0 : top; i <= top && rc == MOE_OK; ++i)
         rc = encode_rows_map(&maps.m[i], int8, a.x, rows, K, gather ? 1u : 16u << i);
     if (rc != MOE_OK) return rc;
     const cudaError_t e = launch_ragged_wide(int8, swiglu, wmap, maps, a, p, stream);

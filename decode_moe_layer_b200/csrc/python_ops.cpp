@@ -5,7 +5,8 @@
 // way there cost 8 to 11 us of host time a call; here it is the launch and little else.
 //
 // Every function takes its arguments by position, None for an absent tensor, enqueues on the current stream of
-// the tensors' device, and returns the outputs, or the C ABI's status as an int if that is not MOE_OK.
+// the tensors' device and returns the outputs.  What the C ABI refuses raises the exception class that operators.py
+// hands over (raise_as).
 #include <Python.h>
 
 #include <ATen/ATen.h>
@@ -139,6 +140,27 @@ long long whole(PyObject *o)
     return v;
 }
 
+PyObject *error_class = nullptr;   // called as error_class(status, function)
+
+PyObject *failed(int status, const char *function)
+{
+    PyObject *e = error_class ? PyObject_CallFunction(error_class, "is", status, function) : nullptr;
+    if (e) {
+        PyErr_SetObject(error_class, e);
+        Py_DECREF(e);
+    } else if (!PyErr_Occurred()) {
+        PyErr_Format(PyExc_RuntimeError, "%s returned %d", function, status);
+    }
+    return nullptr;
+}
+
+PyObject *raise_as(PyObject *, PyObject *cls)
+{
+    Py_INCREF(cls);
+    Py_XSETREF(error_class, cls);
+    Py_RETURN_NONE;
+}
+
 PyObject *count_error(const char *name, Py_ssize_t want, Py_ssize_t got)
 {
     return PyErr_Format(PyExc_TypeError, "%s takes %zd arguments, got %zd", name, want, got);
@@ -198,7 +220,7 @@ PyObject *block_norm(PyObject *, PyObject *const *a, Py_ssize_t n)
     const int rc = moe_block_norm(x.data_ptr(), residual, w_post, gate, kind, w_pre, block_scale, residual_scale, eps,
                                   w_offset, at_of(r), at_of(h), static_cast<int8_t *>(at_of(q)),
                                   static_cast<float *>(at_of(q_s)), size(M), size(H), place.stream);
-    if (rc != MOE_OK) return PyLong_FromLong(rc);
+    if (rc != MOE_OK) return failed(rc, "moe_block_norm");
     return quantize ? wrap_all({&r, &h, &q, &q_s}) : wrap_all({&r, &h});
     MOE_END
 }
@@ -216,7 +238,7 @@ PyObject *int8_quantize(PyObject *, PyObject *const *a, Py_ssize_t n)
     const at::Tensor q = make({M, K}, kI8, dev), s = make({M}, kF32, dev);
     const int rc = moe_int8_quantize(x.data_ptr(), swiglu, static_cast<int8_t *>(q.data_ptr()),
                                      static_cast<float *>(s.data_ptr()), size(M), size(K), place.stream);
-    if (rc != MOE_OK) return PyLong_FromLong(rc);
+    if (rc != MOE_OK) return failed(rc, "moe_int8_quantize");
     return wrap_all({&q, &s});
     MOE_END
 }
@@ -239,7 +261,7 @@ PyObject *int8_gemm(PyObject *, PyObject *const *a, Py_ssize_t n)
     const int rc = moe_int8_gemm(static_cast<const int8_t *>(q.data_ptr()), static_cast<const float *>(q_s),
                                  static_cast<const int8_t *>(w_q), static_cast<const float *>(w_s), add, out.data_ptr(),
                                  f32, size(M), size(N), size(K), static_cast<int32_t *>(status), place.stream);
-    if (rc != MOE_OK) return PyLong_FromLong(rc);
+    if (rc != MOE_OK) return failed(rc, "moe_int8_gemm");
     return THPVariable_Wrap(out);
     MOE_END
 }
@@ -270,7 +292,7 @@ PyObject *grouped_gemm(PyObject *, PyObject *const *a, Py_ssize_t n)
     const int rc = moe_grouped_gemm(x.data_ptr(), wp, static_cast<const int32_t *>(offsets),
                                     static_cast<const int32_t *>(ids), out.data_ptr(), f32, swiglu, size(M), size(N),
                                     size(K), size(E), size(k), static_cast<int32_t *>(status), place.stream);
-    if (rc != MOE_OK) return PyLong_FromLong(rc);
+    if (rc != MOE_OK) return failed(rc, "moe_grouped_gemm");
     return THPVariable_Wrap(out);
     MOE_END
 }
@@ -292,14 +314,15 @@ PyObject *combine(PyObject *, PyObject *const *a, Py_ssize_t n)
     const at::Tensor out = output(a[4], "out", kBf16, {M, H}, dev);
     const int rc = moe_combine(y.data_ptr(), f32, static_cast<const float *>(w), static_cast<const int32_t *>(pos), add,
                                out.data_ptr(), size(M), size(H), size(k), place.stream);
-    if (rc != MOE_OK) return PyLong_FromLong(rc);
+    if (rc != MOE_OK) return failed(rc, "moe_combine");
     return THPVariable_Wrap(out);
     MOE_END
 }
 
 #define MOE_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {MOE_METHOD(block_norm), MOE_METHOD(int8_quantize), MOE_METHOD(int8_gemm),
-                         MOE_METHOD(grouped_gemm), MOE_METHOD(combine), {nullptr, nullptr, 0, nullptr}};
+                         MOE_METHOD(grouped_gemm), MOE_METHOD(combine),
+                         {"raise_as", raise_as, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -92,8 +92,12 @@ __device__ __forceinline__ void mbar_wait_cluster(uint64_t *bar, uint32_t parity
     }
 }
 
-// The box that holds a CTA's half of a tile's tokens: 16 << box rows.
-__device__ __forceinline__ int box_of(int half) { return half <= 16 ? 0 : (half <= 32 ? 1 : (half <= 64 ? 2 : 3)); }
+// The box for a CTA's half of a tile's tokens, 16 << box rows: the smallest that holds them, or with one group, whose
+// tiles are all but one alike, the one for full tiles.
+__device__ __forceinline__ int tile_box(const RaggedArgs &a, int half)
+{
+    return a.offsets != nullptr ? rwide::box_of(half) : rwide::box_of(a.nt / 2);
+}
 
 // Where a warp is in the ring of stages.
 struct Ring {
@@ -163,7 +167,7 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
 
     if (warp == 0 && lane == 0) {
         prefetch_tensormap(&wmap);
-        prefetch_tensormap(&xmaps.m[0]);
+        prefetch_tensormap(&xmaps.m[kGather ? 0 : rwide::box_of(a.nt / 2)]);
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
@@ -207,7 +211,7 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             // weight rows past the expert's last come from the next one, or are zeros: nobody stores their products
             const int wrow = kSwiglu ? w.e * 2 * a.N + block * 64 : w.e * a.N + block * kRows;
             // of both CTAs, weights and tokens
-            const uint32_t bytes = 2 * (kABytes + (kGather ? half : 16 << box_of(half)) * kStageKBytes);
+            const uint32_t bytes = 2 * (kABytes + (kGather ? half : 16 << tile_box(a, half)) * kStageKBytes);
             for (int kb = kb0; kb < kb1; ++kb, ring.next(), ++issued) {
                 mbar_wait(&empty[ring.s], ring.parity ^ 1, aborted, status);
                 aborted = __any_sync(0xffffffffu, aborted);
@@ -240,7 +244,7 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         // ------------------------------------------------------------ tokens: one box of 16, 32, 64 or 128 rows
         Ring ring(a.stages);
         for (; w.locate(); w.next()) {
-            const int half = ((w.count + 31) & ~31) >> 1, box = box_of(half), row0 = w.p0 + half_id * half;
+            const int half = ((w.count + 31) & ~31) >> 1, box = tile_box(a, half), row0 = w.p0 + half_id * half;
             for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
                 mbar_wait(&empty[ring.s], ring.parity ^ 1, aborted, status);
                 aborted = __any_sync(0xffffffffu, aborted);

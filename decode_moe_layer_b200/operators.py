@@ -16,20 +16,16 @@ load()
 from . import _ops  # noqa: E402  (resolves its symbols in libmoe.so)
 
 
-def _run(name, fn, args):
-    res = fn(*args)
-    if type(res) is int:
-        raise MoEError(res, name)
-    return res
+_ops.raise_as(MoEError)
 
 
-def _on(stream, name, fn, args):
+def _on(stream, fn, *args):
     """fn on `stream`: its outputs come from that stream's pool, its tensors are recorded on it."""
     dev = args[0].device if isinstance(args[0], torch.Tensor) else None
     if dev is not None and stream.device != dev:
         raise ValueError("stream is on %s, the tensors are on %s" % (stream.device, dev))
     with torch.cuda.stream(stream):
-        res = _run(name, fn, args)
+        res = fn(*args)
     for t in args:
         if isinstance(t, torch.Tensor):
             t.record_stream(stream)
@@ -53,27 +49,28 @@ def moe_block_norm(x, residual=None, w_post=None, gate=None, w_pre=None, eps=1e-
     (r', h, codes int8 [M,H], scales fp32 [M]).  Without residual, gate, w_post and block_scale, r' would be a copy
     of x: it is then only written where res_out asks for it, and returned as None otherwise.
     res_out and h_out may be x or residual itself."""
-    args = (x, residual, w_post, gate, w_pre, eps, residual_scale, block_scale, w_offset, quantize, res_out, h_out)
     if stream is not None:
-        return _on(stream, "moe_block_norm", _ops.block_norm, args)
-    return _run("moe_block_norm", _ops.block_norm, args)
+        return _on(stream, _ops.block_norm, x, residual, w_post, gate, w_pre, eps, residual_scale, block_scale, w_offset,
+                   quantize, res_out, h_out)
+    return _ops.block_norm(x, residual, w_post, gate, w_pre, eps, residual_scale, block_scale, w_offset, quantize,
+                           res_out, h_out)
 
 
 def moe_int8_quantize(x, swiglu=False, stream=None):
     """(codes int8 [M,K], scales fp32 [M]) of the rows of x bf16 [M,K], or, swiglu=True, of clamp-SwiGLU of
     x = [gate | up] bf16 [M,2K]."""
     if stream is not None:
-        return _on(stream, "moe_int8_quantize", _ops.int8_quantize, (x, swiglu))
-    return _run("moe_int8_quantize", _ops.int8_quantize, (x, swiglu))
+        return _on(stream, _ops.int8_quantize, x, swiglu)
+    return _ops.int8_quantize(x, swiglu)
 
 
 def moe_int8_gemm(q, q_s, w_q, w_s, add=None, out=None, out_dtype=torch.bfloat16, status_out=None, stream=None):
     """q_s[m] * w_s[n] * sum_c q[m,c] w_q[n,c] (+ add): q int8 [M,K], q_s fp32 [M], w_q int8 [N,K], w_s fp32 [N],
     add bf16 [M,N] -> [M,N] in out_dtype (bf16 or fp32).  A bf16 out may be add itself."""
-    args = (q, q_s, w_q, w_s, add, out, _wants_f32(out_dtype), status_out)
+    f32 = _wants_f32(out_dtype)
     if stream is not None:
-        return _on(stream, "moe_int8_gemm", _ops.int8_gemm, args)
-    return _run("moe_int8_gemm", _ops.int8_gemm, args)
+        return _on(stream, _ops.int8_gemm, q, q_s, w_q, w_s, add, out, f32, status_out)
+    return _ops.int8_gemm(q, q_s, w_q, w_s, add, out, f32, status_out)
 
 
 def moe_grouped_gemm(x, w, expert_offsets, sorted_ids=None, k=1, swiglu=False, out=None, out_dtype=torch.bfloat16,
@@ -84,15 +81,15 @@ def moe_grouped_gemm(x, w, expert_offsets, sorted_ids=None, k=1, swiglu=False, o
     int32 [M*k] (moe_permute's), x is bf16 [M,K] and row(p) = sorted_ids[p] // k; without, x is bf16 [R,K] in
     grouped order.  -> [R,N] in out_dtype (bf16 or fp32); positions that no expert's range holds keep what
     `out` held."""
-    args = (x, w, expert_offsets, sorted_ids, k, swiglu, out, _wants_f32(out_dtype), status_out)
+    f32 = _wants_f32(out_dtype)
     if stream is not None:
-        return _on(stream, "moe_grouped_gemm", _ops.grouped_gemm, args)
-    return _run("moe_grouped_gemm", _ops.grouped_gemm, args)
+        return _on(stream, _ops.grouped_gemm, x, w, expert_offsets, sorted_ids, k, swiglu, out, f32, status_out)
+    return _ops.grouped_gemm(x, w, expert_offsets, sorted_ids, k, swiglu, out, f32, status_out)
 
 
 def moe_combine(y, topk_w, inv_pos, add=None, out=None, stream=None):
     """out[t] = sum_j topk_w[t,j] * y[inv_pos[t*k+j]] (+ add[t]), bf16 [M,H]: y bf16 or fp32 [M*k,H] in expert-grouped
     order, topk_w fp32 [M,k], inv_pos int32 [M*k] (moe_permute's).  out may be add itself."""
     if stream is not None:
-        return _on(stream, "moe_combine", _ops.combine, (y, topk_w, inv_pos, add, out))
-    return _run("moe_combine", _ops.combine, (y, topk_w, inv_pos, add, out))
+        return _on(stream, _ops.combine, y, topk_w, inv_pos, add, out)
+    return _ops.combine(y, topk_w, inv_pos, add, out)
