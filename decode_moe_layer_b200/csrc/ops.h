@@ -46,9 +46,9 @@ struct RaggedArgs {
     int R, M, N, K, E, k;
     int nt, stages, stage_bytes, row_blocks, kblocks, split, ring_bytes, accs, acc_cols;   // ragged_wide.cu
 };
-// Maps of the same rows with boxes of 16, 32, 64 and 128 of them; the first alone, one row high, for the gather.
+// Maps of the same rows with boxes of 16, 32, .. 128 of them; the first alone, one row high, for the gather.
 struct BoxMaps {
-    CUtensorMap m[4];
+    CUtensorMap m[8];
 };
 cudaError_t launch_ragged_wide(bool int8, bool swiglu, const CUtensorMap &wmap, const BoxMaps &xmaps,
                                const RaggedArgs &a, const RaggedPlan &p, cudaStream_t s);

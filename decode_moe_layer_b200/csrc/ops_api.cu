@@ -57,9 +57,9 @@ static int run_ragged(bool int8, bool swiglu, const void *w, uint64_t w_rows, Ra
     BoxMaps maps;
     const uint64_t rows = static_cast<uint64_t>(a.M), K = static_cast<uint64_t>(a.K);
     int rc = encode_rows_map(&wmap, int8, w, w_rows, K, swiglu ? 64 : 128);
-    const int top = gather ? 0 : rwide::box_of(p.nt / 2);
+    const int top = gather ? 0 : p.nt / 32 - 1;
     for (int i = a.offsets != nullptr ? 0 : top; i <= top && rc == MOE_OK; ++i)
-        rc = encode_rows_map(&maps.m[i], int8, a.x, rows, K, gather ? 1u : 16u << i);
+        rc = encode_rows_map(&maps.m[i], int8, a.x, rows, K, gather ? 1u : 16u * (i + 1));
     if (rc != MOE_OK) return rc;
     const cudaError_t e = launch_ragged_wide(int8, swiglu, wmap, maps, a, p, stream);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e);

@@ -46,8 +46,7 @@ constexpr int kOffGroups = kOffScales + 8192;             // or, swiglu, what ga
 static_assert(2 * kNt * 4 <= 8192 && 2 * 4 * 8 * 32 * 4 <= 8192, "either fits");
 constexpr int kEpi0 = 4, kGather0 = 8, kGatherWarps = 8;
 constexpr int threads_of(bool gather) { return 32 * (gather ? kGather0 + kGatherWarps : kGather0); }
-// the box of 16 << box_of(rows) token rows that holds so many
-constexpr __host__ __device__ int box_of(int rows) { return rows <= 16 ? 0 : (rows <= 32 ? 1 : (rows <= 64 ? 2 : 3)); }
+constexpr int kRun = 8;                                   // token tiles of a group that run beside each other
 // split: partial sums in runs of 8 columns x 128 rows
 constexpr int kRunBytes = 8 * kRows * 4;
 constexpr int kMaxSplit = 4;                              // pairs per cluster
@@ -78,7 +77,7 @@ inline RaggedPlan wide_plan(int R, int N, int K, int E, bool int8, bool swiglu, 
     long long best = -1;
     for (int tokens = least; tokens == least || (E == 1 && tokens * pair_blocks <= kPlanSMs && tokens * 32 <= R + 31); ++tokens) {
         const int nt = tokens == least ? widest : ((R + tokens - 1) / tokens + 31) / 32 * 32;
-        const int stage = kABytes + (16 << box_of(nt / 2)) * kStageKBytes, cycles = stage / 60 > 2 * nt ? stage / 60 : 2 * nt;
+        const int stage = kABytes + nt / 2 * kStageKBytes, cycles = stage / 60 > 2 * nt ? stage / 60 : 2 * nt;
         const long long tiles = static_cast<long long>(tokens) * pair_blocks;
         for (int split = 1; split <= kMaxSplit; split *= 2) {
             const int need = split > 1 ? split * ((nt / 8 + split - 1) / split) * kRunBytes : 0;   // partial sums

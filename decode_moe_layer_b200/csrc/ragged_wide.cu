@@ -25,8 +25,9 @@
 // The tensor maps have two dimensions: boxes of a map with three or more came in at 10.6 TB/s from L2 over the whole
 // chip, those of a flat one at 16.9, and a TMA instruction costs about 100 cycles whatever its size, so boxes are as
 // high as the tile allows.
-// Tiles go round-robin over the clusters: experts in order, for each its blocks of weight rows, for each its
-// token tiles, so the tiles that run together share operands in L2.
+// Tiles go round-robin over the clusters: experts in order, for each its token tiles by eight, with them the blocks of
+// weight rows, so the tiles that run together are as many in either direction and share operands in L2 (one group of
+// 16384 rows x 4096 x 7168 took 935 us in long runs with all 64 token tiles inside, against HBM and the power limit).
 #include <atomic>
 
 #include "ragged.cuh"
@@ -92,12 +93,9 @@ __device__ __forceinline__ void mbar_wait_cluster(uint64_t *bar, uint32_t parity
     }
 }
 
-// The box for a CTA's half of a tile's tokens, 16 << box rows: the smallest that holds them, or with one group, whose
-// tiles are all but one alike, the one for full tiles.
-__device__ __forceinline__ int tile_box(const RaggedArgs &a, int half)
-{
-    return a.offsets != nullptr ? rwide::box_of(half) : rwide::box_of(a.nt / 2);
-}
+// Token rows of the box for a CTA's half of a tile: just those, or with one group, whose tiles are all but one alike,
+// those of a full tile.
+__device__ __forceinline__ int box_rows(const RaggedArgs &a, int half) { return a.offsets != nullptr ? half : a.nt / 2; }
 
 // Where a warp is in the ring of stages.
 struct Ring {
@@ -127,10 +125,13 @@ struct TileWalk {
     {
         if (t >= total) return false;
         while (t >= first[e + 1] * pair_blocks) ++e;
+        // a group's token tiles in runs of up to kRun; for each run the blocks of weight rows, for each its tiles
         const int tiles = first[e + 1] - first[e], local = t - first[e] * pair_blocks;
-        rb = local / tiles;
+        const int run = local / (rwide::kRun * pair_blocks), in_run = local - run * rwide::kRun * pair_blocks;
+        const int width = min(rwide::kRun, tiles - run * rwide::kRun);
+        rb = in_run / width;
         const int rows = tile_rows(lo[e + 1] - lo[e], nt);
-        p0 = lo[e] + (local - rb * tiles) * rows;
+        p0 = lo[e] + (run * rwide::kRun + in_run - rb * width) * rows;
         count = min(rows, lo[e + 1] - p0);
         return true;
     }
@@ -167,7 +168,7 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
 
     if (warp == 0 && lane == 0) {
         prefetch_tensormap(&wmap);
-        prefetch_tensormap(&xmaps.m[kGather ? 0 : rwide::box_of(a.nt / 2)]);
+        prefetch_tensormap(&xmaps.m[kGather ? 0 : a.nt / 32 - 1]);
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
@@ -211,7 +212,7 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             // weight rows past the expert's last come from the next one, or are zeros: nobody stores their products
             const int wrow = kSwiglu ? w.e * 2 * a.N + block * 64 : w.e * a.N + block * kRows;
             // of both CTAs, weights and tokens
-            const uint32_t bytes = 2 * (kABytes + (kGather ? half : 16 << tile_box(a, half)) * kStageKBytes);
+            const uint32_t bytes = 2 * (kABytes + (kGather ? half : box_rows(a, half)) * kStageKBytes);
             for (int kb = kb0; kb < kb1; ++kb, ring.next(), ++issued) {
                 mbar_wait(&empty[ring.s], ring.parity ^ 1, aborted, status);
                 aborted = __any_sync(0xffffffffu, aborted);
@@ -241,17 +242,17 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 mbar_wait_drain(&full[back % a.stages], (back / a.stages) & 1, status);
             }
     } else if (!kGather && warp == 2) {
-        // ------------------------------------------------------------ tokens: one box of 16, 32, 64 or 128 rows
+        // ------------------------------------------------------------ tokens: one box
         Ring ring(a.stages);
         for (; w.locate(); w.next()) {
-            const int half = ((w.count + 31) & ~31) >> 1, box = tile_box(a, half), row0 = w.p0 + half_id * half;
+            const int half = ((w.count + 31) & ~31) >> 1, map = box_rows(a, half) / 16 - 1, row0 = w.p0 + half_id * half;
             for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
                 mbar_wait(&empty[ring.s], ring.parity ^ 1, aborted, status);
                 aborted = __any_sync(0xffffffffu, aborted);
                 if (aborted) break;
                 const uint32_t bar = map_cluster(smem_u32(&full[ring.s]), leader);
                 if (elect_one())
-                    tma_load_2d_pair(smem + ring.s * a.stage_bytes + kABytes, &xmaps.m[box], kb * kStageK, row0, bar);
+                    tma_load_2d_pair(smem + ring.s * a.stage_bytes + kABytes, &xmaps.m[map], kb * kStageK, row0, bar);
                 __syncwarp();
             }
             if (aborted) break;

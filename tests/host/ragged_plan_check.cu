@@ -32,8 +32,7 @@ int main()
                         CHECK(p.stages >= 1 && p.stages <= rwide::kMaxPipe && p.stages * p.stage_bytes <= p.ring_bytes);
                         CHECK(p.stage_bytes % 1024 == 0 && p.ring_bytes % 1024 == 0 && p.smem <= 227 * 1024);
                         // a stage holds the box of half a tile
-                        const int half = p.nt / 2, box = half <= 16 ? 16 : (half <= 32 ? 32 : (half <= 64 ? 64 : 128));
-                        CHECK(p.stage_bytes == rwide::kABytes + box * rwide::kStageKBytes);
+                        CHECK(p.stage_bytes == rwide::kABytes + p.nt / 2 * rwide::kStageKBytes);
                         // tensor memory: a power of two of columns, and no more of it than of shared memory
                         const long long cols = static_cast<long long>(p.accs) * p.acc_cols;
                         CHECK(p.acc_cols >= p.nt && (p.acc_cols & (p.acc_cols - 1)) == 0 && cols <= 512);
