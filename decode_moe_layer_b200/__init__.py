@@ -1,4 +1,4 @@
-"""B200-native routed MXFP4 Mixture-of-Experts layer for LLM decode.
+"""B200-native routed MXFP4 Mixture-of-Experts layer for LLM decode, and the operators around it in a decoder block.
 
 The compute lives in libmoe.so (hand-written CUDA for sm_100a, C ABI in
 include/moe.h); this package is its thin Python binding.  Importing it loads
