@@ -32,12 +32,12 @@ static bool finite_f(float v) { return v - v == 0.0f; }
 // Maps and launch of a ragged product whose arguments have been checked: w [w_rows][K], x [a.M][K].
 static int run_ragged(bool int8, bool swiglu, const void *w, uint64_t w_rows, RaggedArgs &a, cudaStream_t stream)
 {
-    if (a.status_out) {
-        const cudaError_t e = cudaMemsetAsync(a.status_out, 0, sizeof(int32_t), stream);
-        if (e != cudaSuccess) return cuda_fail(e);
-    }
+    auto clear_status = [&]() {   // last before the launch: a call that fails has enqueued nothing
+        return a.status_out ? cudaMemsetAsync(a.status_out, 0, sizeof(int32_t), stream) : cudaSuccess;
+    };
     if (ragged_by_rows(a.R, a.E, int8)) {
-        const cudaError_t e = launch_ragged_rows(int8, swiglu, w, a, stream);
+        cudaError_t e = clear_status();
+        if (e == cudaSuccess) e = launch_ragged_rows(int8, swiglu, w, a, stream);
         return e == cudaSuccess ? MOE_OK : cuda_fail(e);
     }
     const bool gather = a.sorted_ids != nullptr;
@@ -54,14 +54,15 @@ static int run_ragged(bool int8, bool swiglu, const void *w, uint64_t w_rows, Ra
     // weight boxes of 128 rows, or (swiglu) of 64 gate rows and of 64 up rows; token boxes of the heights that tiles
     // can have
     CUtensorMap wmap;
-    BoxMaps maps;
+    BoxMaps maps = {};
     const uint64_t rows = static_cast<uint64_t>(a.M), K = static_cast<uint64_t>(a.K);
     int rc = encode_rows_map(&wmap, int8, w, w_rows, K, swiglu ? 64 : 128);
     const int top = gather ? 0 : p.nt / 32 - 1;
     for (int i = a.offsets != nullptr ? 0 : top; i <= top && rc == MOE_OK; ++i)
         rc = encode_rows_map(&maps.m[i], int8, a.x, rows, K, gather ? 1u : 16u * (i + 1));
     if (rc != MOE_OK) return rc;
-    const cudaError_t e = launch_ragged_wide(int8, swiglu, wmap, maps, a, p, stream);
+    cudaError_t e = clear_status();
+    if (e == cudaSuccess) e = launch_ragged_wide(int8, swiglu, wmap, maps, a, p, stream);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e);
 }
 

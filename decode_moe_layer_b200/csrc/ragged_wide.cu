@@ -443,6 +443,7 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         }
     }
     __syncwarp();
+    aborted = __any_sync(0xffffffffu, aborted);
     tc_fence_before();
     // Neither CTA ends while the other's MMAs read it.  What a CTA sent to another has been waited for there, so nothing
     // needs ordering; a warp that gave up on a wait cannot know, and orders everything.

@@ -594,3 +594,68 @@ def test_binding_refusals(moe):
 class _FakeStream:
     def __init__(self, device):
         self.device = device
+
+
+# ------------------------------------------------------------------ more than 2^31 elements
+
+def _room(gib):
+    if torch.cuda.mem_get_info()[0] < gib * 2 ** 30:
+        pytest.skip("needs %d GiB of device memory" % gib)
+
+
+def test_outputs_beyond_32_bit_offsets(moe):
+    _room(40)
+    g = gen(20)
+    # int8 product: 40000 x 60000 outputs
+    M, N, K = 40000, 60000, 32
+    q, w = ints(g, -9, 9, M, K, dtype=torch.int8), ints(g, -9, 9, N, K, dtype=torch.int8)
+    one = torch.ones(max(M, N), device="cuda")
+    y = moe.moe_int8_gemm(q, one[:M], w, one[:N])
+    for rows in (slice(0, 3), slice(M - 300, M)):
+        assert torch.equal(y[rows], (q[rows].to(D) @ w.to(D).T).to(F32).to(BF))
+    del y
+    # grouped: 300000 rows of 8192, three groups
+    R, N, K = 300000, 8192, 64
+    x, w = ints(g, -4, 4, R, K), ints(g, -4, 4, 3, N, K)
+    off = torch.tensor([0, 5, 290000, R], dtype=torch.int32, device="cuda")
+    y = moe.moe_grouped_gemm(x, w, off)
+    for e, lo, hi in ((0, 0, 5), (1, 289500, 290000), (2, 290000, 290300), (2, R - 300, R)):
+        assert torch.equal(y[lo:hi], (x[lo:hi].to(D) @ w[e].to(D).T).to(F32).to(BF))
+    # combine takes those rows in reverse, two a token
+    inv = torch.arange(R - 1, -1, -1, dtype=torch.int32, device="cuda")
+    tw = torch.rand(R // 2, 2, generator=g, device="cuda")
+    out = moe.moe_combine(y, tw, inv)
+    t = torch.tensor([0, 1, R // 2 - 1], device="cuda")
+    ref = sum(y[inv[2 * t + j].long()].to(D) * tw[t, j].to(D)[:, None] for j in range(2))
+    mag = sum((y[inv[2 * t + j].long()].to(D) * tw[t, j].to(D)[:, None]).abs() for j in range(2))
+    close(out[t], ref, 2.0 ** -8 * ref.abs() + 3 * 2.0 ** -24 * mag + 1e-30)
+    del out
+    # norm and codes of the same rows
+    wn = randn(g, N)
+    r, h = moe.moe_block_norm(y, residual=y, w_pre=wn)
+    rows = slice(R - 200, R)
+    r2, h2 = moe.moe_block_norm(y[rows].contiguous(), residual=y[rows].contiguous(), w_pre=wn)
+    close(r[rows], r2.to(D), 2.0 ** -7 * r2.to(D).abs() + 1e-30)
+    close(h[rows], h2.to(D), 2.0 ** -7 * h2.to(D).abs() + 2.0 ** -16)
+    del r, h
+    q, s = moe.moe_int8_quantize(y)
+    rq, rs = quant_ref(y[rows].float().cpu())
+    assert torch.equal(q[rows].cpu(), rq) and torch.equal(s[rows].cpu(), rs)
+
+
+@pytest.mark.parametrize("M", [1, 40])
+def test_weights_beyond_32_bit_offsets(moe, M):
+    _room(20)
+    g = gen(21)
+    E, N, K, k = 40, 8192, 8192, 2
+    w = torch.zeros(E, N, K, device="cuda", dtype=BF)
+    w[E - 1] = ints(g, -4, 4, N, K)
+    w[E - 2] = ints(g, -4, 4, N, K)
+    x = ints(g, -4, 4, M, K)
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[E - 1] = M
+    off[E] = 2 * M
+    ids = torch.cat([torch.arange(M) * 2, torch.arange(M) * 2 + 1]).int().cuda()
+    y = moe.moe_grouped_gemm(x, w, off, ids, k=k)
+    assert torch.equal(y[:M], (x.to(D) @ w[E - 2].to(D).T).to(F32).to(BF))
+    assert torch.equal(y[M:], (x.to(D) @ w[E - 1].to(D).T).to(F32).to(BF))
