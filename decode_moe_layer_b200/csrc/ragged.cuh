@@ -129,6 +129,31 @@ __device__ __forceinline__ int block_scan(int v, int *part, Op op)
         if (w < warp) v = op(v, part[w]);
     return v;
 }
+// The table for up to 31 groups by every warp for itself, the same values in the same places: without a barrier, which
+// would cost a small call 0.4 us.
+__device__ __forceinline__ void build_few_groups(const int32_t *off, int R, int E, int nt, int *lo, int *first)
+{
+    const int e = threadIdx.x & 31;
+    int start = e <= E ? min(max(off[e], 0), R) : 0;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, start, d);
+        if (e >= d) start = max(start, v);
+    }
+    const int before = __shfl_up_sync(0xffffffffu, start, 1);
+    int tiles = e > 0 && e <= E ? tile_count(start - before, nt) : 0;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, tiles, d);
+        if (e >= d) tiles += v;
+    }
+    if (e <= E) {
+        lo[e] = start;
+        first[e] = tiles;
+    }
+    __syncwarp();
+}
+
 // The table by a whole CTA of kThreads threads; `lo` and `first` hold E + 1 ints each, `part` 64.  Ends with a barrier.
 template <int kThreads>
 __device__ __forceinline__ void build_groups(const int32_t *off, int R, int E, int nt, int *lo, int *first, int *part)

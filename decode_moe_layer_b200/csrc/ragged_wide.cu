@@ -197,7 +197,12 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     cluster_sync();   // barriers and tensor memory of all CTAs are ready
     tc_fence_after();
     pdl_wait();
-    if (a.offsets != nullptr) build_groups<kThreads>(a.offsets, a.R, a.E, a.nt, lo, first, part);
+    if (a.offsets != nullptr) {
+        if (a.E < 32)
+            build_few_groups(a.offsets, a.R, a.E, a.nt, lo, first);
+        else
+            build_groups<kThreads>(a.offsets, a.R, a.E, a.nt, lo, first, part);
+    }
     pdl_trigger();
     const uint32_t tmem = *tmem_slot;
     bool aborted = false;
