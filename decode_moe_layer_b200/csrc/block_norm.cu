@@ -25,7 +25,8 @@ constexpr int kMaxThreads = 1024;
 constexpr int kRingThreads = 512;   // ring kernel: up to 4 vectors a thread
 constexpr int kMaxStages = 4;
 constexpr int kRingBytes = 200 * 1024;   // of an SM's shared memory, over its CTAs
-constexpr int kRingRows = 4 * kPlanSMs;  // from this many rows on
+constexpr int kRingRows = 4 * kPlanSMs;  // rows from which on the ring kernel runs
+constexpr int kWideVecs = 512;           // wider rows: from the second row of an SM on
 }  // namespace norm
 
 __device__ __forceinline__ void unpack8(uint4 p, float (&f)[8])
@@ -495,7 +496,10 @@ static cudaError_t launch_ring(const NormArgs &a, int threads, cudaStream_t s)
 cudaError_t launch_block_norm(const NormArgs &a, cudaStream_t s)
 {
     const int nvec = a.H / norm::kVec;
-    if (a.M >= norm::kRingRows) {
+    // Without the ring an SM holds several rows at once while a row has at most 512 threads, and one after another
+    // beyond.  Both sides (without, with the ring): 7168 columns, 148 rows 3.2 and 3.7 us, 200 rows 5.4 and 4.6, 590
+    // rows 10.4 and 6.7; 16384 columns, 200 rows 8.0 and 7.3; 2048 columns, 200 rows 2.3 and 3.5, 590 rows 3.5 and 3.9
+    if (a.M >= norm::kRingRows || (nvec > norm::kWideVecs && a.M > kPlanSMs)) {
         // few threads with several vectors each: the reductions cost less, more CTAs hide them (16384 rows of 2048:
         // 50 us with four vectors a thread, 62 with one)
         return nvec <= 64 ? launch_ring<2>(a, row_threads(nvec, 2), s) : launch_ring<4>(a, row_threads(nvec, 4), s);

@@ -68,7 +68,8 @@ def norm_ref(x, residual, w_post, gate, w_pre, eps, rs, bs, off):
 
 
 @pytest.mark.parametrize("M,H", [(1, 8), (1, 7168), (3, 264), (5, 1000), (33, 2048), (2, 8192), (2, 8200), (7, 16384),
-                                 (700, 512), (600, 4104), (593, 16384), (1500, 1024)])
+                                 (700, 512), (600, 4104), (593, 16384), (1500, 1024), (148, 4104), (149, 4104),
+                                 (149, 4096), (200, 7168), (149, 16384)])
 @pytest.mark.parametrize("gate", ["none", "channel", "token", "full"])
 @pytest.mark.parametrize("post,res,pre", [(True, True, True), (False, True, True), (True, False, True),
                                           (True, True, False), (False, False, True)])
