@@ -4,7 +4,8 @@ block, int8 products for its shared expert, bf16 experts grouped by the routing.
 Argument marshalling only, most of it compiled (csrc/python_ops.cpp, built as _ops next to libmoe.so).  All
 tensors of a call are on one CUDA device, which need not be the current one; the work is enqueued on that
 device's current stream, or on `stream`, in which case outputs are allocated for that stream and inputs are
-recorded on it.  Tensors of another type, shape, layout or device raise ValueError (TypeError if they are no
+recorded on it.  Two new outputs of a call that take up to 1 MB together share one allocation (each is contiguous
+and starts on a multiple of 512 bytes).  Tensors of another type, shape, layout or device raise ValueError (TypeError if they are no
 tensors), what the C ABI refuses raises MoEError."""
 from __future__ import annotations
 

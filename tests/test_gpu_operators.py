@@ -117,6 +117,33 @@ def test_block_norm_in_place_and_plain(moe):
     assert torch.equal(y, x) and torch.equal(h, h2)
 
 
+@pytest.mark.parametrize("M,H", [(1, 264), (3, 1000), (31, 8192), (32, 8192), (33, 8192), (64, 16384), (0, 64)])
+def test_outputs_of_a_call_do_not_meet(moe, M, H):
+    # up to 1 MB two outputs share an allocation, beyond each has its own
+    g = gen(M + H)
+    x, r, w = randn(g, M, H), randn(g, M, H), randn(g, H)
+    quant = H % 16 == 0
+    outs = moe.moe_block_norm(x, residual=r, w_pre=w, quantize=quant)
+    outs += moe.moe_int8_quantize(x) if quant else ()
+    for i, t in enumerate(outs):
+        assert t.is_contiguous() and t.data_ptr() % 16 == 0
+        assert t.shape == ((M,) if t.dtype == F32 else (M, H))
+        others = [o.clone() for o in outs]
+        if t.numel() > 0:
+            assert t.storage_offset() * t.element_size() + t.numel() * t.element_size() <= t.untyped_storage().nbytes()
+        keep = t.clone()
+        t.fill_(17)
+        for j, o in enumerate(outs):
+            assert j == i or torch.equal(o, others[j])
+        t.copy_(keep)
+    small = 0 < (M * H * 2 + 511) // 512 * 512 + M * H * 2 <= 1 << 20
+    assert (outs[0].untyped_storage().data_ptr() == outs[1].untyped_storage().data_ptr()) == (small or M == 0)
+    # one output alone is not kept from its place by the other's
+    a = outs[0].clone()
+    h = moe.moe_block_norm(x, residual=r, w_pre=w, res_out=outs[0])[1]
+    assert torch.equal(a, outs[0]) and torch.equal(h, outs[1])
+
+
 def test_block_norm_token_gate_as_column(moe):
     g = gen(8)
     x, r, w = randn(g, 9, 640), randn(g, 9, 640), randn(g, 640)
