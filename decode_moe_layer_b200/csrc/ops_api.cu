@@ -163,6 +163,11 @@ int moe_int8_gemm(const int8_t *q, const float *q_s, const int8_t *w_q, const fl
         ranges_meet(out, on, q_s, static_cast<size_t>(M) * 4) || ranges_meet(out, on, w_s, static_cast<size_t>(N) * 4) ||
         bad_overlap(out, on, add_bf16, mn * 2, out_f32 == 0))
         return MOE_ERR_INVALID_ARG;
+    if (ranges_meet(status_out, 4, out, on) || ranges_meet(status_out, 4, q, static_cast<size_t>(M) * K) ||
+        ranges_meet(status_out, 4, w_q, static_cast<size_t>(N) * K) ||
+        ranges_meet(status_out, 4, q_s, static_cast<size_t>(M) * 4) ||
+        ranges_meet(status_out, 4, w_s, static_cast<size_t>(N) * 4) || ranges_meet(status_out, 4, add_bf16, mn * 2))
+        return MOE_ERR_INVALID_ARG;
     RaggedArgs a = {};
     a.x = q;
     a.K = K;
@@ -200,6 +205,10 @@ int moe_grouped_gemm(const void *x_bf16, const void *w_bf16, const int32_t *expe
     const size_t wn = uE * uN * uK * (swiglu ? 4 : 2);
     if (ranges_meet(y, yn, x_bf16, static_cast<size_t>(x_rows) * K * 2) || ranges_meet(y, yn, w_bf16, wn) ||
         ranges_meet(y, yn, expert_offsets, (uE + 1) * 4) || ranges_meet(y, yn, sorted_ids, static_cast<size_t>(R) * 4))
+        return MOE_ERR_INVALID_ARG;
+    if (ranges_meet(status_out, 4, y, yn) || ranges_meet(status_out, 4, x_bf16, static_cast<size_t>(x_rows) * K * 2) ||
+        ranges_meet(status_out, 4, w_bf16, wn) || ranges_meet(status_out, 4, expert_offsets, (uE + 1) * 4) ||
+        ranges_meet(status_out, 4, sorted_ids, static_cast<size_t>(R) * 4))
         return MOE_ERR_INVALID_ARG;
     RaggedArgs a = {};
     a.offsets = expert_offsets;

@@ -86,6 +86,17 @@ def test_grouped_refusals():
         assert gg(**kw) == UNS, kw
 
 
+def test_status_words_inside_the_operands_are_refused():
+    # the status is cleared before the kernel reads its operands
+    lib, n = moe.load(), (lambda v: P(v) if v else None)
+    for st in (0x100000, 0x200004, 0x300000 + 512 * 2048 - 4, 0x900010, 0xA00000, 0xB00000):
+        assert lib.moe_int8_gemm(n(0x100000), n(0x200000), n(0x300000), n(0x900000), n(0xB00000), n(0xA00000), 0, 8, 512,
+                                 2048, n(st), None) == INV, hex(st)
+    for st in (0x100000, 0x10000000, 0x200000 + 16 * 4, 0x300000, 0x400000 + 32 * 512 * 2 - 4):
+        assert lib.moe_grouped_gemm(n(0x100000), n(0x10000000), n(0x200000), n(0x300000), n(0x400000), 0, 0, 8, 512, 1024,
+                                    16, 4, n(st), None) == INV, hex(st)
+
+
 def test_combine_refusals():
     lib = moe.load()
 
