@@ -1,5 +1,5 @@
 // ops.h -- declarations of the operators around the routed layer: block norms and int8 codes
-// (block_norm.cu), ragged products (ragged_gemm.cu), the weighted combine of expert rows
+// (block_norm.cu), ragged products (ragged_wide.cu, ragged_rows.cu), the weighted combine of expert rows
 // (combine.cu).  Their C entry points are in ops_api.cu.  Not part of the public ABI.
 #pragma once
 

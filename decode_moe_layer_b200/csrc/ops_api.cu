@@ -58,6 +58,9 @@ static int run_ragged(bool int8, bool swiglu, const void *w, uint64_t w_rows, Ra
     const uint64_t rows = static_cast<uint64_t>(a.M), K = static_cast<uint64_t>(a.K);
     int rc = encode_rows_map(&wmap, int8, w, w_rows, K, swiglu ? 64 : 128);
     const int top = gather ? 0 : p.nt / 32 - 1;
+    if (a.offsets == nullptr && rc == MOE_OK &&
+        rwide::halve_last_wave((a.R + p.nt - 1) / p.nt * ((p.row_blocks + 1) / 2), p.clusters, p.nt))
+        rc = encode_rows_map(&maps.m[3], int8, a.x, rows, K, rwide::kNt / 4);
     for (int i = a.offsets != nullptr ? 0 : top; i <= top && rc == MOE_OK; ++i)
         rc = encode_rows_map(&maps.m[i], int8, a.x, rows, K, gather ? 1u : 16u * (i + 1));
     if (rc != MOE_OK) return rc;

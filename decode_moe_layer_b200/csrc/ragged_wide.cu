@@ -94,8 +94,11 @@ __device__ __forceinline__ void mbar_wait_cluster(uint64_t *bar, uint32_t parity
 }
 
 // Token rows of the box for a CTA's half of a tile: just those, or with one group, whose tiles are all but one alike,
-// those of a full tile.
-__device__ __forceinline__ int box_rows(const RaggedArgs &a, int half) { return a.offsets != nullptr ? half : a.nt / 2; }
+// those of a full tile or of half a one.
+__device__ __forceinline__ int box_rows(const RaggedArgs &a, int half, bool halved)
+{
+    return a.offsets != nullptr ? half : (halved ? rwide::kNt / 4 : a.nt / 2);
+}
 
 // Where a warp is in the ring of stages.
 struct Ring {
@@ -114,25 +117,43 @@ struct Ring {
 // The tiles of one cluster, in order: t = cluster, cluster + clusters, ...
 struct TileWalk {
     const int *lo, *first;
-    int nt, pair_blocks, total, step, t, e;
+    int nt, pair_blocks, whole, end, step, t, e;   // from t = whole on, halves of tiles
     int rb, p0, count;   // of the current tile
+    bool halved;
     __device__ __forceinline__ TileWalk(const int *lo_, const int *first_, const RaggedArgs &a, int start, int step_)
-        : lo(lo_), first(first_), nt(a.nt), pair_blocks((a.row_blocks + 1) >> 1), total(first_[a.E] * pair_blocks),
-          step(step_), t(start), e(0)
+        : lo(lo_), first(first_), nt(a.nt), pair_blocks((a.row_blocks + 1) >> 1), whole(first_[a.E] * pair_blocks),
+          end(whole), step(step_), t(start), e(0), halved(false)
     {
+        if (rwide::halve_last_wave(whole, step, nt)) {
+            const int last = whole % step;
+            whole -= last;
+            end += last;
+        }
     }
     __device__ __forceinline__ bool locate()
     {
-        if (t >= total) return false;
-        while (t >= first[e + 1] * pair_blocks) ++e;
+        if (t >= end) return false;
+        const int tail = t - whole, tile = tail < 0 ? t : whole + (tail >> 1);
+        while (tile >= first[e + 1] * pair_blocks) ++e;
         // a group's token tiles in runs of up to kRun; for each run the blocks of weight rows, for each its tiles
-        const int tiles = first[e + 1] - first[e], local = t - first[e] * pair_blocks;
+        const int tiles = first[e + 1] - first[e], local = tile - first[e] * pair_blocks;
         const int run = local / (rwide::kRun * pair_blocks), in_run = local - run * rwide::kRun * pair_blocks;
         const int width = min(rwide::kRun, tiles - run * rwide::kRun);
         rb = in_run / width;
         const int rows = tile_rows(lo[e + 1] - lo[e], nt);
         p0 = lo[e] + (run * rwide::kRun + in_run - rb * width) * rows;
         count = min(rows, lo[e + 1] - p0);
+        if (tail >= 0) {
+            halved = count > rwide::kNt / 2;
+            if (!halved) return (tail & 1) == 0;   // (no cluster has another tile behind it)
+            const int part = (((count + 1) >> 1) + 31) & ~31;
+            if (tail & 1) {
+                p0 += part;
+                count -= part;
+            } else {
+                count = part;
+            }
+        }
         return true;
     }
     __device__ __forceinline__ void next() { t += step; }
@@ -217,7 +238,7 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             // weight rows past the expert's last come from the next one, or are zeros: nobody stores their products
             const int wrow = kSwiglu ? w.e * 2 * a.N + block * 64 : w.e * a.N + block * kRows;
             // of both CTAs, weights and tokens
-            const uint32_t bytes = 2 * (kABytes + (kGather ? half : box_rows(a, half)) * kStageKBytes);
+            const uint32_t bytes = 2 * (kABytes + (kGather ? half : box_rows(a, half, w.halved)) * kStageKBytes);
             for (int kb = kb0; kb < kb1; ++kb, ring.next(), ++issued) {
                 mbar_wait(&empty[ring.s], ring.parity ^ 1, aborted, status);
                 aborted = __any_sync(0xffffffffu, aborted);
@@ -250,7 +271,7 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         // ------------------------------------------------------------ tokens: one box
         Ring ring(a.stages);
         for (; w.locate(); w.next()) {
-            const int half = ((w.count + 31) & ~31) >> 1, map = box_rows(a, half) / 16 - 1, row0 = w.p0 + half_id * half;
+            const int half = ((w.count + 31) & ~31) >> 1, map = box_rows(a, half, w.halved) / 16 - 1, row0 = w.p0 + half_id * half;
             for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
                 mbar_wait(&empty[ring.s], ring.parity ^ 1, aborted, status);
                 aborted = __any_sync(0xffffffffu, aborted);

@@ -244,6 +244,45 @@ def test_int8_gemm_largest_sums(moe):
     assert torch.equal(y.to(D), ref)
 
 
+# Calls of more tiles than CTA pairs (74) whose last wave is less than half full: its tiles run as two halves each.
+@pytest.mark.parametrize("M,N", [(2500, 4096), (2354, 4096), (2560, 4000), (1100, 8192), (4096, 4096), (20000, 512)])
+def test_int8_gemm_last_wave(moe, M, N):
+    g = gen(M + N)
+    K = 400
+    q, w = ints(g, -128, 127, M, K, dtype=torch.int8), ints(g, -128, 127, N, K, dtype=torch.int8)
+    one = torch.ones(max(M, N), device="cuda")
+    y = moe.moe_int8_gemm(q, one[:M], w, one[:N], out_dtype=F32)
+    assert torch.equal(y.to(D), q.to(D) @ w.to(D).T)     # sums below 2^24: exact in fp32
+
+
+@pytest.mark.parametrize("cuts,N", [([0, 300, 300, 812, 1200], 4096), ([0, 1100], 8192), ([7, 250, 2600, 2600, 2616], 4096),
+                                    ([0, 129, 258, 387, 516, 3000], 2048), ([0, 20, 700, 740, 996, 996], 5000)])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_grouped_gemm_last_wave(moe, cuts, N, gather, swiglu):
+    R, E, K = cuts[-1] + 9, len(cuts) - 1, 136
+    g = gen(R + N + E)
+    if swiglu:
+        N //= 2
+    x, w = ints(g, -4, 4, R, K), ints(g, -4, 4, E, 2 * N if swiglu else N, K)
+    off = torch.tensor(cuts, dtype=torch.int32, device="cuda")
+    ids = torch.randperm(R, generator=g, device="cuda").int() if gather else None
+    out = torch.full((R, N), 5.0, device="cuda")
+    y = moe.moe_grouped_gemm(x, w, off, ids, k=1, swiglu=swiglu, out=out, out_dtype=F32)
+    assert (y[:cuts[0]] == 5).all() and (y[cuts[-1]:] == 5).all()
+    for e in range(E):
+        lo, hi = cuts[e], cuts[e + 1]
+        p = (x[ids[lo:hi].long()] if gather else x[lo:hi]).to(D) @ w[e].to(D).T
+        if not swiglu:
+            assert torch.equal(y[lo:hi].to(D), p)
+            continue
+        a, u = p[:, :N].clamp(max=7), p[:, N:].clamp(-7, 7)
+        ref = a * torch.sigmoid(a) * u
+        # the sums are exact; exp, the division and two products are off by a few units of 2^-24 each, exp's argument is
+        # at most 16 K, but where it is large and negative the value is below 2^-100
+        close(y[lo:hi], ref, 2.0 ** -20 * ref.abs() + 2.0 ** -100, "group %d" % e)
+
+
 # ------------------------------------------------------------------ grouped
 
 def grouping(g, M, k, E, how):
