@@ -5,7 +5,7 @@
 // works on the last; products and sums on the ordinary pipes (fp32 FMA; dp4a into int32), a warp reduction at the
 // end of a row.  No tensor map, barrier, cluster or tensor memory: what a call of this size waits for is the launch,
 // one trip to memory and the stream of the weights; the tensor-core kernel's set-up costs it 3 to 4 us more (int8, one
-// token, weights out of L2: 1536 x 2048 1.9 against 5.9 us, 4096 x 7168 6.4 against 9.8; the weights alone 0.5 and
+// token, weights out of L2: 1536 x 2048 1.9 against 5.9 us, 4096 x 7168 7.1 against 9.8; the weights alone 0.5 and
 // 4.5).  8 of 128 experts of 1536 x 2048 with a row each: 10.4 us, 50 MB.
 // With several groups a tile is one position of the grouped order, whose group a warp counts out of the offsets; rows
 // of the same group then read its weights from L2 again, which is why groups of more than a row or so go to the tiles
@@ -21,6 +21,10 @@ constexpr int kWarps = 4;
 constexpr int rows_of(bool int8, int t) { return int8 && t > 1 ? 4 : 2; }
 constexpr int runs_of(bool int8, int t) { return int8 && t > 1 ? 2 : 4; }
 constexpr int kWarpsPerSm = 64;   // aimed at: more than an SM holds, so that SMs that are done early find work
+// weights up to here are asked for whole ahead of the call's dependency; several tokens, which take longer, gain from
+// that only with small ones (4 tokens and their codes, 7168 x 2048: whole 7.8 us, first loads 7.4, none 7.8; 512 x 7168:
+// 9.7, 10.1, 10.1)
+constexpr uint32_t ahead_bytes(int t) { return (t == 1 ? 32u : 8u) << 20; }
 }  // namespace rrows
 
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
@@ -43,6 +47,8 @@ __device__ __forceinline__ void dot16(int &acc, uint4 w, uint4 x)
     acc = __dp4a(static_cast<int>(w.z), static_cast<int>(x.z), acc);
     acc = __dp4a(static_cast<int>(w.w), static_cast<int>(x.w), acc);
 }
+
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 template <bool kInt8>
 struct RowAcc {
@@ -67,6 +73,21 @@ ragged_rows_kernel(const void *wbase, const __grid_constant__ RaggedArgs a, int 
     // the warp's steps: columns n_first, + n_next, .. below a.N
     const int n_first = (rb * steps * kWarps + warp) * kCols, n_next = kWarps * kCols;
     if (n_first >= a.N) return;
+    if (a.offsets == nullptr) {
+        // What the warp reads first, into L2 while the kernel before (that makes the codes, say) still runs: its rows, or
+        // of larger weights what its first loads bring.  Codes and product of one token in a run of calls, 4096 x 7168,
+        // 8.4 against 7.5 us, 16384 x 7168 20.1 against 18.3 (with whole rows 22.1).  Into L2 only: that kernel may still
+        // write the weights.
+        const uint32_t row_bytes = static_cast<uint32_t>(a.K) * (kInt8 ? 1 : 2), rows = min(kW, a.N - n_first);
+        const char *w = static_cast<const char *>(wbase) + static_cast<size_t>(n_first) * row_bytes;
+        if (static_cast<uint64_t>(gridDim.x) * kWarps * kW * row_bytes <= ahead_bytes(kT)) {
+            for (uint32_t b = lane * 128u; b < rows * row_bytes; b += 4096u) prefetch_l2(w + b);
+        } else {
+            constexpr uint32_t kLines = 4 * kRuns;   // of 128 bytes, in each row
+            const uint32_t r = lane / kLines, b = lane % kLines * 128u;
+            if (r < rows && b < row_bytes) prefetch_l2(w + static_cast<size_t>(r) * row_bytes + b);
+        }
+    }
     pdl_wait();
     pdl_trigger();
     int expert = 0, p0 = tt * kT, count = min(kT, a.R - p0);
