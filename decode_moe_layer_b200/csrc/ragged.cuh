@@ -80,9 +80,11 @@ __device__ __forceinline__ uint32_t map_cluster(uint32_t smem_addr, uint32_t ran
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr), "r"(rank));
     return remote;
 }
-__device__ __forceinline__ void st_cluster4(uint32_t cluster_addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+// Stores 16 bytes in another CTA's shared memory and reports them to that CTA's barrier as they land.
+__device__ __forceinline__ void st_async4(uint32_t cluster_addr, const uint32_t *v, uint32_t cluster_bar)
 {
-    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(a), "r"(b), "r"(c), "r"(d)
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.u32 [%0], {%1, %2, %3, %4}, [%5];"
+                 ::"r"(cluster_addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(cluster_bar)
                  : "memory");
 }
 
