@@ -29,20 +29,23 @@ __device__ __forceinline__ uint32_t umma_idesc_i8(int m, int n)
 }
 
 // D (+)= A * B^T over 32 bytes of K by the CTA pair: kind::f16 (16 bf16 elements) or kind::i8 (32 int8 elements).
-// Issued by the pair's even CTA; each CTA holds half of A's rows and half of B's.
+// Issued by the pair's even CTA; each CTA holds half of A's rows and half of B's.  a, b: the low words of the
+// operands' descriptors (umma_sdesc_sw128), which hold the address; hi: the high word of both.
 template <bool kInt8>
-__device__ __forceinline__ void umma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+__device__ __forceinline__ void umma_pair(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc,
                                           uint32_t accumulate)
 {
     if (kInt8)
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-                     "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+                     "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+                     "tcgen05.mma.cta_group::2.kind::i8 [%0], da, db, %4, p;\n\t}" ::"r"(d_tmem),
+                     "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(accumulate)
                      : "memory");
     else
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-                     "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+                     "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+                     "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d_tmem),
+                     "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(accumulate)
                      : "memory");
 }
 

@@ -35,22 +35,22 @@
 
 namespace moe {
 
-// Copies that complete on a barrier of either CTA of the pair (bar: cluster address).
-__device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map, int c0, int c1, uint32_t bar)
+// Copies that complete on a barrier of either CTA of the pair (dst: shared-memory, bar: cluster address).
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar)
 {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
         "[%1, {%2, %3}], [%4];"
-        ::"r"(smem_u32(dst)), "l"(map), "r"(c0), "r"(c1), "r"(bar)
+        ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(bar)
         : "memory");
 }
-__device__ __forceinline__ void tma_gather4_pair(void *dst, const CUtensorMap *map, int c0, const int (&r)[4],
+__device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const CUtensorMap *map, int c0, const int (&r)[4],
                                                  uint32_t bar)
 {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
         "[%1, {%2, %3, %4, %5, %6}], [%7];"
-        ::"r"(smem_u32(dst)), "l"(map), "r"(c0), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar)
+        ::"r"(dst), "l"(map), "r"(c0), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar)
         : "memory");
 }
 // One arrival on the barrier at the same place in both CTAs of the pair once the MMAs issued before are complete.
@@ -93,13 +93,36 @@ __device__ __forceinline__ void mbar_wait_cluster(uint64_t *bar, uint32_t parity
     }
 }
 
-// The same for a whole warp, with one answer for all its lanes; a barrier that is through costs one try and a vote.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, bool &aborted, const StatusPtrs &st)
+// A whole warp's wait for copies, or MMAs, with one answer for all its lanes (bar: shared-memory address).
+__device__ __forceinline__ bool warp_try_wait(uint32_t bar, uint32_t parity)
 {
-    if (__all_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity))) return true;
-    mbar_wait_cluster(bar, parity, aborted, st);
-    aborted = __any_sync(0xffffffffu, aborted);
-    return !aborted;
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "vote.sync.all.pred q, p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, bool &aborted, const StatusPtrs &st)
+{
+    if (warp_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!warp_try_wait(bar, parity)) {
+        if (__any_sync(0xffffffffu, clock64() - t0 > kWaitLimitCycles)) {
+            aborted = true;
+            record_timeout(st);
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
 // Token rows of the box for a CTA's half of a tile: just those, or with one group, whose tiles are all but one alike,
@@ -109,15 +132,17 @@ __device__ __forceinline__ int box_rows(const RaggedArgs &a, int half, bool halv
     return a.offsets != nullptr ? half : (halved ? rwide::kNt / 4 : a.nt / 2);
 }
 
-// Where a warp is in the ring of stages.
+// Where a warp is in the ring of stages: bytes to the stage and to its barriers.  The loops over stages keep to few
+// instructions: with 64 tokens a stage's MMAs take 128 cycles, and the issuing warp @@.
 struct Ring {
-    int n, s = 0;
-    uint32_t parity = 0;
-    __device__ __forceinline__ explicit Ring(int stages) : n(stages) {}
+    uint32_t stage_bytes, bars, at = 0, bar = 0, parity = 0;
+    __device__ __forceinline__ explicit Ring(const RaggedArgs &a) : stage_bytes(a.stage_bytes), bars(8 * a.stages) {}
     __device__ __forceinline__ void next()
     {
-        if (++s == n) {
-            s = 0;
+        at += stage_bytes;
+        bar += 8;
+        if (bar == bars) {
+            at = bar = 0;
             parity ^= 1;
         }
     }
@@ -244,13 +269,14 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     const TileWalk tile0 = w;
     const bool any = more;
     const bool elected = elect_one();
-    const uint32_t full0 = map_cluster(smem_u32(full), leader);
+    const uint32_t ring0 = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty);
+    const uint32_t full_pair = map_cluster(full0, leader);
     if (a.offsets == nullptr) pdl_wait();   // (one group: all of the above is ready by then)
     pdl_trigger();
 
     if (warp == 0) {
         // ------------------------------------------------------------ weights
-        Ring ring(a.stages);
+        Ring ring(a);
         int issued = 0;
         for (; more && !aborted; w.next(), more = w.locate()) {
             const int half = ((w.count + 31) & ~31) >> 1, block = 2 * w.rb + half_id;
@@ -259,24 +285,20 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             // of both CTAs, weights and tokens
             const uint32_t bytes = 2 * (kABytes + (kGather ? half : box_rows(a, half, w.halved)) * kStageKBytes);
             for (int kb = kb0; kb < kb1; ++kb, ring.next(), ++issued) {
-                if (!warp_wait(&empty[ring.s], ring.parity ^ 1, aborted, status)) break;
-                uint8_t *sa = smem + ring.s * a.stage_bytes;
-                const uint32_t bar = full0 + 8 * ring.s;
+                if (!warp_wait(empty0 + ring.bar, ring.parity ^ 1, aborted, status)) break;
+                const uint32_t sa = ring0 + ring.at, bar = full_pair + ring.bar;
                 if (elected) {
-                    if (half_id == 0) mbar_arrive_expect_tx(&full[ring.s], bytes);
+                    if (half_id == 0) expect_tx(full0 + ring.bar, bytes);
                     tma_load_2d_pair(sa, &wmap, kb * kStageK, wrow, bar);   // swiglu: 64 gate rows, then their up rows
                     if (kSwiglu) tma_load_2d_pair(sa + kABytes / 2, &wmap, kb * kStageK, wrow + a.N, bar);
                 }
-                __syncwarp();
             }
         }
         // the MMA warp's releases of the last stages arrive while this CTA lives
-        if (issued >= a.stages) {
-            for (int i = 0; i < a.stages; ++i, ring.next())
-                mbar_wait(&empty[ring.s], ring.parity ^ 1, aborted, status);
-        } else {
-            for (int i = 0; i < issued; ++i) mbar_wait(&empty[i], 0, aborted, status);
-        }
+        __syncwarp();
+        const int filled = min(issued, a.stages);
+        for (int i = issued - filled; i < issued && !aborted; ++i)
+            warp_wait(empty0 + 8 * (i % a.stages), (i / a.stages) & 1, aborted, status);
         // after a timeout the even CTA waits for both CTAs' copies in flight: the stages before the one it gave up on
         if (aborted && half_id == 0)
             for (int i = 0; i < a.stages && i < issued; ++i) {
@@ -285,42 +307,41 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             }
     } else if (!kGather && warp == 2) {
         // ------------------------------------------------------------ tokens: one box
-        Ring ring(a.stages);
+        Ring ring(a);
         for (; more && !aborted; w.next(), more = w.locate()) {
             const int half = ((w.count + 31) & ~31) >> 1, map = box_rows(a, half, w.halved) / 16 - 1, row0 = w.p0 + half_id * half;
             for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
-                if (!warp_wait(&empty[ring.s], ring.parity ^ 1, aborted, status)) break;
+                if (!warp_wait(empty0 + ring.bar, ring.parity ^ 1, aborted, status)) break;
                 if (elected)
-                    tma_load_2d_pair(smem + ring.s * a.stage_bytes + kABytes, &xmaps.m[map], kb * kStageK, row0,
-                                     full0 + 8 * ring.s);
-                __syncwarp();
+                    tma_load_2d_pair(ring0 + ring.at + kABytes, &xmaps.m[map], kb * kStageK, row0, full_pair + ring.bar);
             }
         }
     } else if (warp == 1 && half_id == 0) {
         // ------------------------------------------------------------ MMA issuer
-        Ring ring(a.stages);
+        Ring ring(a);
+        const uint64_t desc = umma_sdesc_sw128(ring0);
+        const uint32_t desc_lo = static_cast<uint32_t>(desc), desc_hi = static_cast<uint32_t>(desc >> 32);
         int i = 0;
         for (; more && !aborted; w.next(), more = w.locate(), ++i) {
             const int b = a.accs > 1 ? i & 1 : 0, n32 = (w.count + 31) & ~31;
             const uint32_t idesc = kInt8 ? umma_idesc_i8(256, n32) : umma_idesc_bf16(256, n32);
             const uint32_t acc = tmem + b * a.acc_cols;
-            warp_wait(&acc_empty[b], ((i >> 1) & 1) ^ 1, aborted, status);
+            if (!warp_wait(smem_u32(&acc_empty[b]), ((i >> 1) & 1) ^ 1, aborted, status)) break;
             for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
-                if (!warp_wait(&full[ring.s], ring.parity, aborted, status)) break;
+                if (!warp_wait(full0 + ring.bar, ring.parity, aborted, status)) break;
                 tc_fence_after();
-                const uint32_t sa = smem_u32(smem + ring.s * a.stage_bytes);
-                const uint64_t ad = umma_sdesc_sw128(sa), bd = umma_sdesc_sw128(sa + kABytes);
+                const uint32_t ad = desc_lo + (ring.at >> 4), bd = ad + (kABytes >> 4);
                 if (elected) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) umma_pair<kInt8>(acc, ad + 2 * j, bd + 2 * j, idesc, kb > kb0 || j > 0);
-                    umma_commit_pair(smem_u32(&empty[ring.s]), leader);
+                    for (int j = 0; j < 4; ++j)
+                        umma_pair<kInt8>(acc, ad + 2 * j, bd + 2 * j, desc_hi, idesc, kb > kb0 || j > 0);
+                    umma_commit_pair(empty0 + ring.bar, leader);
                 }
-                __syncwarp();
             }
             if (aborted) break;
             if (elected) umma_commit_pair(smem_u32(&acc_full[b]), leader);
-            __syncwarp();
         }
+        __syncwarp();
         // the epilogues' last arrivals, of the other CTA too, land while this CTA lives
         if (split == 1)
             for (int j = i > 1 ? i - 2 : 0; j < i; ++j)
@@ -380,7 +401,7 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         // ------------------------------------------------------------ gather
         // Runs of four rows go round the warps, lane i of warp g taking run g + 8 i.
         const int g = warp - kGather0;
-        Ring ring(a.stages);
+        Ring ring(a);
         for (; more; w.next(), more = w.locate()) {
             const int half = ((w.count + 31) & ~31) >> 1;
             const int run = g + kGatherWarps * lane;
@@ -393,10 +414,10 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 idx[i] = static_cast<int>(min(f / static_cast<uint32_t>(a.k), static_cast<uint32_t>(a.M - 1)));
             }
             for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
-                if (!warp_wait(&empty[ring.s], ring.parity ^ 1, aborted, status)) break;
+                if (!warp_wait(empty0 + ring.bar, ring.parity ^ 1, aborted, status)) break;
                 if (mine)
-                    tma_gather4_pair(smem + ring.s * a.stage_bytes + kABytes + run * 4 * kStageKBytes, &xmaps.m[0],
-                                     kb * kStageK, idx, full0 + 8 * ring.s);
+                    tma_gather4_pair(ring0 + ring.at + kABytes + run * 4 * kStageKBytes, &xmaps.m[0], kb * kStageK, idx,
+                                     full_pair + ring.bar);
                 __syncwarp();
             }
             if (aborted) break;
