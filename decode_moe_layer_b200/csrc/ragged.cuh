@@ -58,6 +58,16 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8])
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[8]) { tmem_ld8(taddr, v); }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[16]) { tmem_ld16(taddr, v); }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&v)[4])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
 // ------------------------------------------------------------------ clusters
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -204,14 +214,27 @@ __device__ __forceinline__ void store_pair(const RaggedArgs &a, float g, float u
         static_cast<__nv_bfloat16 *>(a.y)[at] = __float2bfloat16_rn(h);
 }
 
+// The addend of kCols columns as finish_columns takes it.  The loads are unconditional, the last live column's again
+// past it: behind branches they go out one after the other.
+template <bool kInt8, int kCols>
+__device__ __forceinline__ void load_add(const RaggedArgs &a, size_t row, int live, int n, __nv_bfloat16 (&t)[kCols])
+{
+    if (!kInt8 || a.add == nullptr || n >= a.N || live <= 0) return;
+    const size_t ld = static_cast<size_t>(a.N);
+    const __nv_bfloat16 *add = a.add + row * ld + n;
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) t[j] = add[min(j, live - 1) * ld];
+}
+
 // Finishes kCols accumulator columns (consecutive rows of y from `row`, of which `live` are the tile's) of
-// the weight row n: scales and adds (int8: rs[] the rows' scales, cs the channel's), rounds once and stores.
+// the weight row n: scales and adds (int8: rs[] the rows' scales, cs the channel's, t[] the addend), rounds once and
+// stores.
 // For a column a warp writes 64 consecutive bytes (bf16), whole sectors.  The common case, all columns live,
 // has no branch between columns: a thread's chain of address, conversion and store took about 120 cycles a
 // column when each column branched, and a fifth of that without.
 template <bool kInt8, int kCols>
 __device__ __forceinline__ void finish_columns(const RaggedArgs &a, const uint32_t (&v)[kCols], const float *rs, float cs,
-                                               size_t row, int live, int n)
+                                               const __nv_bfloat16 *t, size_t row, int live, int n)
 {
     if (n >= a.N) return;
     const size_t ld = static_cast<size_t>(a.N);
@@ -221,10 +244,6 @@ __device__ __forceinline__ void finish_columns(const RaggedArgs &a, const uint32
     for (int j = 0; j < kCols; ++j)
         f[j] = kInt8 ? static_cast<float>(static_cast<int32_t>(v[j])) * rs[j] * cs : __uint_as_float(v[j]);
     if (kInt8 && a.add != nullptr) {
-        const __nv_bfloat16 *add = a.add + at;
-        __nv_bfloat16 t[kCols];
-#pragma unroll
-        for (int j = 0; j < kCols; ++j) t[j] = j < live ? add[j * ld] : __float2bfloat16_rn(0.f);
 #pragma unroll
         for (int j = 0; j < kCols; ++j) f[j] += __bfloat162float(t[j]);
     }

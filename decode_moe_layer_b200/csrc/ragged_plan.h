@@ -46,6 +46,7 @@ constexpr int kOffGroups = kOffScales + 8192;             // or, swiglu, what ga
 static_assert(2 * kNt * 4 <= 8192 && 2 * 4 * 8 * 32 * 4 <= 8192, "either fits");
 constexpr int kEpi0 = 4, kGather0 = 8, kGatherWarps = 8;
 constexpr int threads_of(bool gather) { return 32 * (gather ? kGather0 + kGatherWarps : kGather0); }
+constexpr int kEpiCols = 16;                              // columns of an accumulator that a thread finishes together
 constexpr int kRun = 8;                                   // token tiles of a group that run beside each other
 // split: partial sums in runs of 8 columns x 128 rows
 constexpr int kRunBytes = 8 * kRows * 4;

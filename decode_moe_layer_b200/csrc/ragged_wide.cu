@@ -361,7 +361,7 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 for (int j = threadIdx.x - 32 * kEpi0; j < kNt; j += 128) rs[j] = j < w.count ? a.row_scale[w.p0 + j] : 0.f;
                 asm volatile("bar.sync 1, 128;" ::: "memory");
             }
-            mbar_wait_cluster(&acc_full[b], (i >> 1) & 1, aborted, status);
+            mbar_wait(&acc_full[b], (i >> 1) & 1, aborted, status);
             tc_fence_after();
             // (after a timeout the rest runs on whatever is there: the warps keep meeting at their barriers)
             const uint32_t acc = tmem + b * a.acc_cols + (static_cast<uint32_t>(32 * q) << 16);
@@ -384,13 +384,16 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                         h[j] = __float_as_uint(ragged_swiglu(up ? other : own, up ? own : other));
                     }
                     const int c0 = c + 8 * up;
-                    finish_columns<false, 8>(a, h, nullptr, 1.0f, static_cast<size_t>(w.p0) + c0, w.count - c0, ns);
+                    finish_columns<false, 8>(a, h, nullptr, 1.0f, nullptr, static_cast<size_t>(w.p0) + c0, w.count - c0, ns);
                 }
             } else {
-                for (int c = 0; c < w.count; c += 16) {
-                    uint32_t v[16];
-                    tmem_ld16(acc + c, v);
-                    finish_columns<kInt8, 16>(a, v, rs + c, cs, static_cast<size_t>(w.p0) + c, w.count - c, n);
+                for (int c = 0; c < w.count; c += kEpiCols) {
+                    const size_t row = static_cast<size_t>(w.p0) + c;
+                    __nv_bfloat16 add[kEpiCols];
+                    load_add<kInt8>(a, row, w.count - c, n, add);
+                    uint32_t v[kEpiCols];
+                    tmem_ld(acc + c, v);
+                    finish_columns<kInt8, kEpiCols>(a, v, rs + c, cs, add, row, w.count - c, n);
                 }
             }
             tc_fence_before();
@@ -437,14 +440,25 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         const int runs = found ? (t.count + 7) >> 3 : 0, own = (runs + split - 1) / split;
         const int group = warp >> 2, row = 32 * (warp & 3) + lane;
         if (found) {
-            mbar_wait_cluster(&acc_full[0], 0, aborted, status);
+            const int block = 2 * t.rb + half_id;
+            const int n = block * kRows + row;
+            float cs = 1.0f;
+            __nv_bfloat16 add[8];
+            if (kInt8) {   // all that the end needs from memory
+                if (n < a.N) cs = a.col_scale[n];
+                if (threadIdx.x < kNt) scales[threadIdx.x] = threadIdx.x < t.count ? a.row_scale[t.p0 + threadIdx.x] : 0.f;
+                const int c = 8 * (group * split + slice);
+                load_add<kInt8>(a, static_cast<size_t>(t.p0) + c, t.count - c, n, add);
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+            }
+            mbar_wait(&acc_full[0], 0, aborted, status);
             tc_fence_after();
             if (warp == 0 && lane < split)
                 mbar_arrive_cluster_relaxed(map_cluster(smem_u32(free_all), static_cast<uint32_t>(2 * lane + half_id)));
             if (warp == 1 && lane == 0)
                 mbar_arrive_expect_tx(landed, static_cast<uint32_t>((runs - slice + split - 1) / split * split * kRunBytes));
             __syncwarp();
-            mbar_wait_cluster(free_all, 0, aborted, status);
+            mbar_wait(free_all, 0, aborted, status);
             __syncwarp();
             const uint32_t acc = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
             for (int u = group; u < runs; u += 2) {
@@ -456,9 +470,6 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 st_async4(at + kRunBytes / 2, v + 4, bar);
             }
             mbar_wait_cluster(landed, 0, aborted, status);
-            const int block = 2 * t.rb + half_id;
-            const int n = block * kRows + row;
-            const float cs = kInt8 && found && n < a.N ? a.col_scale[n] : 1.0f;
             // part of slice s for run i, column half h, accumulator row r
             auto part = [&](int s, int i, int h, int r) {
                 return *reinterpret_cast<const uint4 *>(smem + (s * own + i) * kRunBytes + h * (kRunBytes / 2) + r * 16);
@@ -488,16 +499,13 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         v[j] = __float_as_uint(ragged_swiglu(__uint_as_float(g[j]), __uint_as_float(up[j])));
-                    finish_columns<false, 4>(a, v, nullptr, 1.0f, row0 + 4 * h, live - 4 * h, block * 64 + r);
+                    finish_columns<false, 4>(a, v, nullptr, 1.0f, nullptr, row0 + 4 * h, live - 4 * h, block * 64 + r);
                 } else {
                     uint32_t v[8];
-                    float rs[8];
                     sum(i, 0, row, v);
                     sum(i, 1, row, v + 4);
-                    if (kInt8)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) rs[j] = j < live ? a.row_scale[row0 + j] : 0.f;
-                    finish_columns<kInt8, 8>(a, v, rs, cs, row0, live, n);
+                    finish_columns<kInt8, 8>(a, v, scales + c, cs, add, row0, live, n);
+                    load_add<kInt8>(a, row0 + 16 * split, live - 16 * split, n, add);   // of run i + 2
                 }
             }
         }
