@@ -9,13 +9,13 @@ namespace moe {
 // ------------------------------------------------------------------ by weight rows or by tiles
 
 // Measured on this part (times on the GPU, weights out of L2), by rows against tiles:
-//  * int8: 4096 x 7168 with 1, 2, 4 tokens 6.4, 8.5, 9.7 us against 9.8, with 8 tokens 11.3; 1536 x 2048 with 1, 2, 4
-//    tokens 1.9, 2.8, 3.6 us against 5.9; 7168 x 2048 with 4 tokens 6.1 against 7.1, with 8 9.9.
-//  * grouped, 128 experts of 1536 x 2048, top-8: 4, 8, 12, 16 tokens 29, 52, 69, 84 us against 37, 56, 68, 79; 256
-//    experts of 7168 x 2048: 8, 16, 20, 32 tokens 235, 414, 495, 727 us against 237, 416, 505, 681.  From about 0.7
-//    rows a group on, groups of two and more rows pay for a tile.
+//  * int8, codes and product: 4096 x 7168 with 4 tokens 11.9 us against 11.5, 1536 x 2048 5.7 against 6.9, 7168 x 2048
+//    7.6 against 8.9; with 8 tokens the rows take about twice their time with 4, the tiles no longer.
+//  * grouped, 128 experts of 1536 x 2048, top-8: 4, 8, 12 tokens 28, 52, 69 us against 35, 53, 67; 256 experts of 7168 x
+//    2048: 8, 16, 20, 32 tokens 235, 414, 495, 727 us against 237, 416, 505, 681.  From about 0.7 rows a group on, groups
+//    of two and more rows pay for a tile.
 //  * with 16 rows at most the call is so short that the tiles' set-up decides: 4 tokens x 4 of 16 experts of 1024 x 1024
-//    6.2 us against 8.5.
+//    7.1 us against 8.4, 1 token 3.7 against 7.4.
 constexpr int kRowsMaxTokens = 4;    // int8
 constexpr int kRowsMaxShort = 16;    // grouped
 inline bool ragged_by_rows(int R, int E, bool int8)
@@ -79,25 +79,27 @@ inline RaggedPlan wide_plan(int R, int N, int K, int E, bool int8, bool swiglu, 
     const int least = E == 1 ? (R + kNt - 1) / kNt : (R < E ? R : E) + (R - 1) / kNt;   // token tiles of up to 256
     const int widest = R < kNt ? (R + 31) / 32 * 32 : kNt;
     // Token tiles and pairs per cluster by the estimated cycles of the longest cluster: waves x stages x a stage (its
-    // bytes at 60 a cycle, or its MMAs), the last tile's columns (20 cycles each) and, if pairs share a tile, the
-    // joining (2500 and 40 a column).  More, narrower tiles than `least` only for a single group, whose size the host
+    // bytes at 60 a cycle, half as many where two CTAs share an SM, or its MMAs), the last tile's columns (20 cycles each)
+    // and, if pairs share a tile, the joining (1200 and 42 a column).  More, narrower tiles than `least` only for a single group, whose size the host
     // knows.  Where two CTAs fit an SM, 33 clusters of eight or 71 of four run at once, else 15 or 33.
-    // Measured (int8, 4096 x 7168): 16 tokens by four pairs a tile 9.8 us, by one 16; 256 tokens as four tiles of 64 by two
-    // pairs 15, as one by four 20, as one by one 23.
+    // Measured (int8): 33 tokens x 1536 x 2048 by four pairs a tile 5.5 us, by one 6.0, 128 tokens 6.7 and 5.9; 8 x 7168 x
+    // 2048 by four pairs (two CTAs an SM) 7.3, by one 6.7; 256 tokens x 4096 x 7168 as four tiles of 64 by two pairs 15.
     long long best = -1;
     for (int tokens = least; tokens == least || (E == 1 && tokens * pair_blocks <= kPlanSMs && tokens * 32 <= R + 31); ++tokens) {
         const int nt = tokens == least ? widest : ((R + tokens - 1) / tokens + 31) / 32 * 32;
-        const int stage = kABytes + nt / 2 * kStageKBytes, cycles = stage / 60 > 2 * nt ? stage / 60 : 2 * nt;
+        const int stage = kABytes + nt / 2 * kStageKBytes;
         const long long tiles = static_cast<long long>(tokens) * pair_blocks;
         for (int split = 1; split <= kMaxSplit; split *= 2) {
             const int need = split > 1 ? split * ((nt / 8 + split - 1) / split) * kRunBytes : 0;   // partial sums
             const bool twice = need <= kHalfSmBytes;
             const int fit = split == 4 ? (twice ? 33 : 15) : (split == 2 ? (twice ? 71 : 33) : kPlanSMs / 2);
-            if (split > 1 && (tiles > fit || p.kblocks < 4 * split)) continue;
+            if (split > 1 && (tiles > fit || p.kblocks < 2 * split)) continue;
+            const int copies = stage / 60 * (tiles * split > kPlanSMs / 2 && split > 1 ? 2 : 1);
+            const int cycles = copies > 2 * nt ? copies : 2 * nt;
             const int slice = (p.kblocks + split - 1) / split;
             const bool halves = E == 1 && halve_last_wave(static_cast<int>(tiles), fit, nt);
             const long long cost = (tiles + fit - 1) / fit * slice * cycles - (halves ? slice * (cycles / 4) : 0) + 20 * nt +
-                                   (split > 1 ? 2500 + 40 * nt : 0);
+                                   (split > 1 ? 1200 + 42 * nt : 0);
             if (best >= 0 && cost >= best) continue;
             best = cost;
             // a cluster with one tile at most: one accumulator, no more stages than it can use, and (narrow tiles) half an

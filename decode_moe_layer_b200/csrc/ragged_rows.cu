@@ -4,8 +4,8 @@
 // kW rows at a time (swiglu: a gate row and its up row), the next eight loads of a lane always on their way while it
 // works on the last; products and sums on the ordinary pipes (fp32 FMA; dp4a into int32), a warp reduction at the
 // end of a row.  No tensor map, barrier, cluster or tensor memory: what a call of this size waits for is the launch,
-// one trip to memory and the stream of the weights; the tensor-core kernel's set-up costs it 3 to 4 us more (int8, one
-// token, weights out of L2: 1536 x 2048 1.9 against 5.9 us, 4096 x 7168 7.1 against 9.8; the weights alone 0.5 and
+// one trip to memory and the stream of the weights; the tensor-core kernel's set-up costs it 2 to 3 us more (int8, one
+// token, weights out of L2: 1536 x 2048 1.9 against 4.8 us, 4096 x 7168 7.1 against 8.8; the weights alone 0.5 and
 // 4.5).  8 of 128 experts of 1536 x 2048 with a row each: 10.4 us, 50 MB.
 // With several groups a tile is one position of the grouped order, whose group a warp counts out of the offsets; rows
 // of the same group then read its weights from L2 again, which is why groups of more than a row or so go to the tiles
