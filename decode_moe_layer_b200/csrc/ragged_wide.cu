@@ -283,7 +283,7 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             // weight rows past the expert's last come from the next one, or are zeros: nobody stores their products
             const int wrow = kSwiglu ? w.e * 2 * a.N + block * 64 : w.e * a.N + block * kRows;
             // of both CTAs, weights and tokens
-            const uint32_t bytes = 2 * (kABytes + (kGather ? half : box_rows(a, half, w.halved)) * kStageKBytes);
+            const uint32_t bytes = 2 * (kABytes + (kGather ? max(half, 4 * kGatherWarps) : box_rows(a, half, w.halved)) * kStageKBytes);
             for (int kb = kb0; kb < kb1; ++kb, ring.next(), ++issued) {
                 if (!warp_wait(empty0 + ring.bar, ring.parity ^ 1, aborted, status)) break;
                 const uint32_t sa = ring0 + ring.at, bar = full_pair + ring.bar;
@@ -402,13 +402,16 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         }
     } else if (kGather && warp >= kGather0) {
         // ------------------------------------------------------------ gather
-        // Runs of four rows go round the warps, lane i of warp g taking run g + 8 i.
+        // Runs of four rows go round the warps, lane i of warp g taking run g + 8 i.  With 16 rows, four runs, the last
+        // four warps copy them once more: every warp has a part in every stage, since one that only watched could fall
+        // behind by a whole turn of the ring, whose barriers tell two turns apart and no more.
         const int g = warp - kGather0;
         Ring ring(a);
         for (; more; w.next(), more = w.locate()) {
             const int half = ((w.count + 31) & ~31) >> 1;
-            const int run = g + kGatherWarps * lane;
-            const bool mine = 4 * run < half;
+            const int first_run = 4 * g < half ? g : g - half / 4;
+            const int run = first_run + kGatherWarps * lane;
+            const bool mine = 4 * run < half && (lane == 0 || first_run == g);
             int idx[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {

@@ -373,6 +373,19 @@ def test_grouped_gemm_exact_on_integers(moe, M, k, E, N, K, how, gather):
     assert torch.equal(y, ref.to(F32).to(BF))
 
 
+@pytest.mark.parametrize("R,k,E,N,K", [(102, 2, 52, 2883, 1960), (60, 4, 43, 1995, 1576), (700, 2, 40, 1230, 664)])
+def test_gather_of_tiny_and_larger_groups_in_turn(moe, R, k, E, N, K):
+    # groups of less than 17 rows leave warps of the gather without rows; they have to keep in step all the same
+    g = gen(R + E)
+    off, ids, _, _ = grouping(g, R // k, k, E, "skew" if R == 700 else "uniform")
+    x, w = ints(g, -4, 4, R // k, K), ints(g, -4, 4, E, N, K)
+    ref, _ = grouped_ref(x, w, off, ids, k, False)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for _ in range(30):
+        y = moe.moe_grouped_gemm(x, w, off, ids, k=k, out_dtype=F32, status_out=status)
+        assert status.item() == 0 and torch.equal(y.to(D), ref)
+
+
 @pytest.mark.parametrize("R,E,nt_hint", [(40, 8, "narrow"), (3000, 8, "wide")])
 def test_grouped_rows_outside_the_groups_stay(moe, R, E, nt_hint):
     g = gen(R)
