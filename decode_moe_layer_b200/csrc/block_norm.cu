@@ -4,7 +4,7 @@
 //   z  = x * rsqrt(mean(x^2) + eps) * (w_post + o)      (z = x without w_post)
 //   r' = block_scale * gate * z + residual_scale * r     (stored as bf16)
 //   h  = r' * rsqrt(mean(r'^2) + eps) * (w_pre + o)      (stored as bf16 and / or int8 codes)
-//   q  = rne(h / s), s = max|h| / 127 per row
+//   q  = rne(127 h / max|h|), s = max|h| / 127 per row
 //
 // A row stays in the registers of one CTA, so x, r, r' and h each cross HBM once.  All arithmetic is in
 // fp32; r' and h are rounded once, as they are stored, and h is computed from the unrounded r'.  The
@@ -50,22 +50,33 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8])
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The codes rne(v / s) of eight values for the row scale s = max / 127, |code| <= 127; a row of zeros has s = 0 and
-// codes 0.  `inv` is 1 / s.  v * inv is off from the rounded quotient by less than 127 * 2^-22, so the two round to the
-// same integer unless it lies that near to a half: only then (one value in ten thousand) are the quotients taken.
-// Rounded with a division each, the codes took 2.5 times as long as their memory traffic.  Rows so small that 1 / s
-// overflows divide as well.
+// The codes rne(127 v / max) of eight values and the row scale s = max / 127; a row of zeros has s = 0 and codes 0.
+// `inv` is 1 / s.  v * inv is off from the quotient by less than 127 * 2^-22, so the two round to the same integer
+// unless it lies that near to a half (one value in five thousand).  Only then the side of the half is decided, by
+// comparing 254 v with (2 n + 1) max, whose products an FMA completes to all their bits: the rounded s would decide ties
+// at random, and ties are common (bf16 rows hold max / 2, whose code is 63.5).  Rounded with a division each, the codes
+// took 2.5 times as long as their memory traffic.  Rows so small that 1 / s overflows divide by the scale as it is
+// stored, which may be denormal.
 struct CodeScale {
-    float s, inv;
-    __device__ __forceinline__ explicit CodeScale(float max_abs) : s(max_abs / 127.0f), inv(0.f)
+    float s, inv, top;
+    __device__ __forceinline__ explicit CodeScale(float max_abs) : s(max_abs / 127.0f), inv(0.f), top(max_abs)
     {
         if (s > 0x1p-120f) inv = 1.0f / s;
     }
 };
-__device__ __forceinline__ uint32_t int8_code_exact(float v, float s)
+// One such code (not inlined: 32 copies of it cost the quantiser a quarter of its speed).
+__device__ __noinline__ uint32_t int8_code_exact(float v, float s, float inv, float max_abs)
 {
-    const int c = s > 0.f ? __float2int_rn(v / s) : 0;
-    return static_cast<uint32_t>(max(-127, min(127, c)));
+    if (inv == 0.f) {
+        const int c = s > 0.f ? __float2int_rn(v / s) : 0;
+        return static_cast<uint32_t>(max(-127, min(127, c)));
+    }
+    const float t = v * inv, r = rintf(t), n2 = 2.f * r + (t >= r ? 1.f : -1.f);   // n2 / 2: the half next to t
+    const float a = 254.f * 0x1p-8f, top = max_abs * 0x1p-8f;   // (no overflow for the largest rows)
+    const float p = n2 * top, w = a * v;
+    const float d = (w - p) + (fmaf(a, v, -w) - fmaf(n2, top, -p));
+    const float c = d > 0.f ? 0.5f * (n2 + 1.f) : (d < 0.f ? 0.5f * (n2 - 1.f) : rintf(0.5f * n2));
+    return static_cast<uint32_t>(max(-127, min(127, __float2int_rn(c))));
 }
 __device__ __forceinline__ uint2 int8_codes8(const float (&f)[8], const CodeScale &k)
 {
@@ -80,7 +91,10 @@ __device__ __forceinline__ uint2 int8_codes8(const float (&f)[8], const CodeScal
     }
     if (!(far < 0.4999f) || k.inv == 0.f) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] = int8_code_exact(f[i], k.s);
+        for (int i = 0; i < 8; ++i) {
+            const float t = f[i] * k.inv;
+            if (!(fabsf(t - rintf(t)) < 0.4999f) || k.inv == 0.f) c[i] = int8_code_exact(f[i], k.s, k.inv, k.top);
+        }
     }
     return make_uint2(prmt(prmt(c[0], c[1], 0x0040u), prmt(c[2], c[3], 0x0040u), 0x5410u),
                       prmt(prmt(c[4], c[5], 0x0040u), prmt(c[6], c[7], 0x0040u), 0x5410u));

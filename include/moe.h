@@ -306,7 +306,7 @@ int moe_block_norm(const void *x_bf16, const void *residual_bf16, const void *w_
 
 /*
  * Symmetric 8-bit codes of rows, the activations of moe_int8_gemm:
- *   q_s[m] = max_c |v[m,c]| / 127,  q[m,c] = round-half-even(v[m,c] / q_s[m])   (a row of zeros: 0, codes 0)
+ *   q_s[m] = max_c |v[m,c]| / 127,  q[m,c] = round-half-even(127 v[m,c] / max_c |v[m,c]|)   (zeros: 0, codes 0)
  * with v = x (bf16 [M,K]) or, swiglu != 0, v = silu(min(g,7)) * clamp(u,-7,7) of x = [g | u] (bf16 [M,2K]:
  * K gate columns, then K up columns), kept in fp32.  K a multiple of 16, at most 16384.
  */

@@ -170,10 +170,25 @@ def test_block_norm_zero_rows_and_nan_rows(moe):
 # ------------------------------------------------------------------ int8
 
 def quant_ref(v):
-    """Codes as the definition gives them in fp32 (the same divisions and rounding)."""
-    s = v.abs().amax(1) / np.float32(127)
-    q = torch.where(s[:, None] > 0, v / s[:, None], torch.zeros_like(v))
-    return torch.round(q).clamp(-127, 127).to(torch.int8), s
+    """Codes and scales as the definition gives them: 127 v is exact in 64 bits and a tie's quotient too."""
+    top = v.abs().amax(1)
+    q = torch.where(top[:, None] > 0, 127 * v.to(D) / top[:, None].to(D), torch.zeros_like(v, dtype=D))
+    return torch.round(q).to(torch.int8), top / np.float32(127)
+
+
+def test_int8_codes_of_ties(moe):
+    # every bf16 mantissa as a row's largest value: its half has the code 63.5, which goes to the even neighbour whatever
+    # the rounding of the scale; 2 max / 254 * odd is a tie too where bf16 holds it
+    top = (torch.arange(128, 256, device="cuda") * 2.0 ** -3).to(BF)
+    x = torch.zeros(128, 64, dtype=BF, device="cuda")
+    x[:, 0], x[:, 1], x[:, 2] = top, top / 2, -top / 2
+    x[126, 3:35] = (torch.arange(32, device="cuda") * 2 + 1).to(BF) * 2.0 ** -3   # of 254 / 8: codes n + 1/2
+    q, _ = moe.moe_int8_quantize(x)
+    assert (q[:, 0] == 127).all() and (q[:, 1] == 64).all() and (q[:, 2] == -64).all()
+    want = torch.round(torch.arange(32, device="cuda", dtype=D) + 0.5).to(torch.int8)
+    assert torch.equal(q[126, 3:35], want)
+    h = moe.moe_block_norm(x, w_pre=torch.ones(64, dtype=BF, device="cuda"), quantize=True)
+    assert (h[2][:, 1] == -h[2][:, 2]).all() and ((h[2][:, 1] == 63) | (h[2][:, 1] == 64)).all()
 
 
 @pytest.mark.parametrize("M,K", [(1, 16), (1, 7168), (3, 272), (33, 2048), (5, 8208), (2, 16384), (600, 768)])
