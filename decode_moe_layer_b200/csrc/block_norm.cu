@@ -50,7 +50,8 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8])
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The codes rne(127 v / max) of eight values and the row scale s = max / 127; a row of zeros has s = 0 and codes 0.
+// The codes rne(127 v / max) of eight values and the row scale s = max / 127; a row of zeros has s = 0 and codes 0, one
+// with NaN or Inf a scale that is not finite and codes 0.
 // `inv` is 1 / s.  v * inv is off from the quotient by less than 127 * 2^-22, so the two round to the same integer
 // unless it lies that near to a half (one value in five thousand).  Only then the side of the half is decided, by
 // comparing 254 v with (2 n + 1) max, whose products an FMA completes to all their bits: the rounded s would decide ties
@@ -100,14 +101,22 @@ __device__ __forceinline__ uint2 int8_codes8(const float (&f)[8], const CodeScal
                       prmt(prmt(c[4], c[5], 0x0040u), prmt(c[6], c[7], 0x0040u), 0x5410u));
 }
 
-// Sum and maximum of a pair over the CTA; every thread gets both.  `buf` holds one pair per warp and is
+// The larger of two values, NaN if either is (fmaxf would drop it): a row that holds NaN has to have a NaN scale.
+__device__ __forceinline__ float max_or_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Sum and maximum (NaN if there is one) of a pair over the CTA; every thread gets both.  `buf` holds one pair per warp and is
 // free again after the next call's barrier on the other buffer (callers alternate two).
 __device__ __forceinline__ float2 block_sum_max(float sum, float mx, float2 *buf)
 {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
         sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        mx = max_or_nan(mx, __shfl_xor_sync(0xffffffffu, mx, d));
     }
     if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = make_float2(sum, mx);
     __syncthreads();
@@ -118,7 +127,7 @@ __device__ __forceinline__ float2 block_sum_max(float sum, float mx, float2 *buf
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
         sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        mx = max_or_nan(mx, __shfl_xor_sync(0xffffffffu, mx, d));
     }
     return make_float2(sum, mx);
 }
@@ -192,7 +201,7 @@ __global__ void __launch_bounds__(norm::kMaxThreads) block_norm_kernel(const __g
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 v[i][j] *= t[j] + a.w_offset;
-                mx = fmaxf(mx, fabsf(v[i][j]));
+                mx = max_or_nan(mx, fabsf(v[i][j]));
             }
         }
     }
@@ -380,7 +389,7 @@ block_norm_ring_kernel(const __grid_constant__ NormArgs a, int stages)
             for (int j = 0; j < 4; ++j) {
                 ss = fma2(v[i][j], v[i][j], ss);
                 v[i][j] = mul2(v[i][j], f_pre[i][j]);
-                if (kQuant) mx = fmaxf(mx, fmaxf(fabsf(v[i][j].x), fabsf(v[i][j].y)));
+                if (kQuant) mx = max_or_nan(mx, max_or_nan(fabsf(v[i][j].x), fabsf(v[i][j].y)));
             }
         }
         if (has_pre) {
@@ -417,8 +426,9 @@ block_norm_ring_kernel(const __grid_constant__ NormArgs a, int stages)
 // of the value for |g| <= 80, against a code's step of 2^-8 of the row's largest.
 __device__ __forceinline__ float swiglu_fast(float g, float u)
 {
-    const float a = fminf(g, 7.0f);
-    return __fdividef(a, 1.0f + __expf(-a)) * fminf(fmaxf(u, -7.0f), 7.0f);
+    const float a = g > 7.0f ? 7.0f : g;   // (comparisons let a NaN through)
+    const float c = u > 7.0f ? 7.0f : (u < -7.0f ? -7.0f : u);
+    return __fdividef(a, 1.0f + __expf(-a)) * c;
 }
 
 // Codes of the rows of x [M, K], or of clamp-SwiGLU of the rows' halves [gate | up] ([M, 2K], kSwiglu;
@@ -453,7 +463,7 @@ int8_quantize_kernel(const __nv_bfloat16 *x, int8_t *q, float *q_s, int K)
             for (int j = 0; j < 8; ++j) v[i][j] = swiglu_fast(v[i][j], u[j]);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(v[i][j]));
+        for (int j = 0; j < 8; ++j) mx = max_or_nan(mx, fabsf(v[i][j]));
     }
     const CodeScale s(block_sum_max(0.f, mx, red).y);
     if (threadIdx.x == 0) q_s[row] = s.s;

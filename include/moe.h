@@ -276,7 +276,8 @@ int moe_mxfp4_forward_profile(const void *x, const float *router_w, const float 
  * counterpart; these are interface choices of this library.  Conventions as above, and:
  *   - none of them uses a workspace, so calls on different streams and captured graphs share nothing;
  *   - activations bf16, sums in fp32 (int32 for int8 products), one rounding per output;
- *   - NaN and Inf in a row stay in that row's outputs (int8 codes of such a row are undefined);
+ *   - NaN and Inf in a row stay in that row's outputs, and do not get lost on the way through int8: a row of values
+ *     with a NaN among them has the scale NaN, one with an Inf the scale Inf or NaN, and either codes 0;
  *   - outputs may not overlap inputs except where a function says so.
  */
 

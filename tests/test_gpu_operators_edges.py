@@ -1,0 +1,54 @@
+"""The operators around the routed layer where a value is no number, an index is wrong or a wait gives up: against plain
+implementations in 64 bits, with the tolerances of test_gpu_operators.py where none is derived here."""
+import pytest
+import torch
+
+from tests.test_gpu_operators import BF, D, F32, close, gen, int8_ref, ints, moe, quant_ref, randn  # noqa: F401
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
+
+NAN = float("nan")
+
+
+# ------------------------------------------------------------------ int8 codes
+
+# a vector of 8 a thread (M <= 148 and K <= 8192) and four
+@pytest.mark.parametrize("M,K", [(2, 16), (5, 2048), (3, 16384), (149, 768), (200, 8208)])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_nan_reaches_the_scale_of_its_row(moe, M, K, swiglu):
+    g = gen(M + K)
+    x = randn(g, M, 2 * K if swiglu else K, scale=3.0)
+    q0, s0 = moe.moe_int8_quantize(x, swiglu=swiglu)
+    columns = [0, K // 2, K - 1] + ([K, 2 * K - 8] if swiglu else [])    # of swiglu: gate and up
+    for i, c in enumerate(columns):
+        bad, y = (i * 7 + 1) % M, x.clone()
+        y[bad, c] = NAN if i % 2 else -NAN
+        q, s = moe.moe_int8_quantize(y, swiglu=swiglu)
+        keep = torch.arange(M, device="cuda") != bad
+        assert torch.isnan(s[bad]) and (q[bad] == 0).all(), c
+        assert torch.equal(s[keep], s0[keep]) and torch.equal(q[keep], q0[keep])
+        # and, through the product, all of its row and no other
+        n = 5
+        w, ws = ints(g, -9, 9, n, K, dtype=torch.int8), torch.ones(n, device="cuda")
+        for m in (slice(0, M), slice(bad, bad + 1)):      # in tiles (M > 4), by rows
+            y8 = moe.moe_int8_gemm(q[m].contiguous(), s[m].contiguous(), w, ws)
+            assert torch.isnan(y8[keep[m].logical_not()]).all() and torch.isfinite(y8[keep[m]]).all()
+
+
+@pytest.mark.parametrize("M", [3, 160])
+def test_inf_makes_an_infinite_scale_and_codes_of_zero(moe, M):
+    x = randn(gen(M), M, 256)
+    x[1, 17] = -float("inf")
+    q, s = moe.moe_int8_quantize(x)
+    assert s[1] == float("inf") and (q[1] == 0).all() and torch.isfinite(s[0]) and torch.isfinite(s[2:]).all()
+
+
+@pytest.mark.parametrize("M,H", [(3, 512), (700, 512), (200, 4112)])
+def test_norm_codes_of_a_nan_weight(moe, M, H):
+    # the row's sum of squares is finite, one element of h is not
+    g = gen(M)
+    x, w = randn(g, M, H), randn(g, H)
+    w[H - 3] = NAN
+    _, h, q, s = moe.moe_block_norm(x, w_pre=w, quantize=True)
+    assert torch.isnan(s).all() and (q == 0).all()
+    assert torch.isnan(h[:, H - 3]).all() and torch.isfinite(h[:, :H - 3]).all()
