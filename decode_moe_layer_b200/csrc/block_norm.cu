@@ -422,13 +422,16 @@ block_norm_ring_kernel(const __grid_constant__ NormArgs a, int stages)
     }
 }
 
-// silu(min(g, 7)) * clamp(u, -7, 7) for the codes: exp and the division by their fast forms, off by less than 2^-16
-// of the value for |g| <= 80, against a code's step of 2^-8 of the row's largest.
-__device__ __forceinline__ float swiglu_fast(float g, float u)
+// silu(min(g, 7)) * clamp(u, -7, 7) in fp32, NaN for a NaN.  With t = exp(-|a|), silu(a) = a / (1 + t) or a t / (1 + t): the
+// divisor is in [1, 2], where __fdividef is within 2 units in the last place whatever the gate, and no gate overflows exp.
+// All in all 12 * 2^-24 of the value (exp and the division 2 units each, four roundings).  a / (1 + exp(-a)) with its
+// division rounded took 156 us for 16384 x 7168 and 2.00 for 33 x 768; this takes 140 and 1.65.
+__device__ __forceinline__ float swiglu_fp32(float g, float u)
 {
     const float a = g > 7.0f ? 7.0f : g;   // (comparisons let a NaN through)
     const float c = u > 7.0f ? 7.0f : (u < -7.0f ? -7.0f : u);
-    return __fdividef(a, 1.0f + __expf(-a)) * c;
+    const float t = expf(-fabsf(a));
+    return __fdividef(a > 0.0f ? a : a * t, 1.0f + t) * c;
 }
 
 // Codes of the rows of x [M, K], or of clamp-SwiGLU of the rows' halves [gate | up] ([M, 2K], kSwiglu;
@@ -460,7 +463,7 @@ int8_quantize_kernel(const __nv_bfloat16 *x, int8_t *q, float *q_s, int K)
             float u[8];
             unpack8(p[i][kSwiglu ? 1 : 0], u);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = swiglu_fast(v[i][j], u[j]);
+            for (int j = 0; j < 8; ++j) v[i][j] = swiglu_fp32(v[i][j], u[j]);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) mx = max_or_nan(mx, fabsf(v[i][j]));

@@ -52,3 +52,22 @@ def test_norm_codes_of_a_nan_weight(moe, M, H):
     _, h, q, s = moe.moe_block_norm(x, w_pre=w, quantize=True)
     assert torch.isnan(s).all() and (q == 0).all()
     assert torch.isnan(h[:, H - 3]).all() and torch.isfinite(h[:, :H - 3]).all()
+
+
+# exp and the division within 2 units in the last place (2^-22) each, 1 + t, two products and the division by 127 half a
+# unit (2^-24) each: 12 * 2^-24.  At -88 the value is still inside fp32's normal range.
+@pytest.mark.parametrize("gate", [(-88.0, -88.0), (-88.5, -80.0), (-60.0, -20.0), (-20.0, -5.0), (-5.0, 10.0)])
+@pytest.mark.parametrize("M,K", [(4, 64), (200, 512)])
+def test_swiglu_codes_keep_fp32(moe, gate, M, K):
+    g = gen(K)
+    lo, hi = gate
+    x = torch.cat([lo + (hi - lo) * torch.rand(M, K, generator=g, device="cuda"),
+                   3 + 3 * torch.rand(M, K, generator=g, device="cuda")], 1).to(BF)
+    q, s = moe.moe_int8_quantize(x, swiglu=True)
+    a, u = x[:, :K].to(D).clamp(max=7), x[:, K:].to(D).clamp(-7, 7)
+    v = a * torch.sigmoid(a) * u
+    top = v.abs().amax(1)
+    close(s, top / 127, 12 * 2.0 ** -24 * top / 127, "scale")
+    # the code is the nearest of 127 v / max, each of v and max off by as much
+    t = 127 * v / top[:, None]
+    close(q, t, torch.full_like(t, 0.5 + 127 * 24 * 2.0 ** -24), "codes")
