@@ -71,3 +71,17 @@ def test_swiglu_codes_keep_fp32(moe, gate, M, K):
     # the code is the nearest of 127 v / max, each of v and max off by as much
     t = 127 * v / top[:, None]
     close(q, t, torch.full_like(t, 0.5 + 127 * 24 * 2.0 ** -24), "codes")
+
+
+def test_codes_of_tiny_rows(moe):
+    # down to bf16's smallest subnormals, where the row's scale has few bits left or none: 127 v / max all the same
+    g = gen(3)
+    x = torch.randn(64, 272, generator=g, device="cuda", dtype=F32)
+    e = -90.0 - torch.arange(64, device="cuda") * 0.75             # rows of about 2^-90 .. 2^-137
+    x = (x.to(D) * 2.0 ** e.to(D)[:, None]).to(BF)
+    x[:, 1] = x.abs().amax(1)                                      # ties: the code 63.5 (where bf16 holds the half)
+    x[:, 2] = x[:, 1] / 2
+    q, s = moe.moe_int8_quantize(x)
+    rq, rs = quant_ref(x.float().cpu())
+    assert torch.equal(s.cpu(), rs)
+    assert torch.equal(q.cpu(), rq), "rows %s" % (q.cpu() != rq).any(1).nonzero().flatten().tolist()
