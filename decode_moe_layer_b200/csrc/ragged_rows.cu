@@ -7,7 +7,7 @@
 // one trip to memory and the stream of the weights; the tensor-core kernel's set-up costs it 2 to 3 us more (int8, one
 // token, weights out of L2: 1536 x 2048 1.9 against 4.8 us, 4096 x 7168 7.1 against 8.8; the weights alone 0.5 and
 // 4.5).  8 of 128 experts of 1536 x 2048 with a row each: 10.4 us, 50 MB.
-// With several groups a tile is one position of the grouped order, whose group a warp counts out of the offsets; rows
+// With several groups a tile is one position of the grouped order, whose group a warp finds among the offsets; rows
 // of the same group then read its weights from L2 again, which is why groups of more than a row or so go to the tiles
 // (ragged_by_rows, ragged_plan.h).
 // The order of the sums is fixed: lane, then the reduction tree.
@@ -92,10 +92,11 @@ ragged_rows_kernel(const void *wbase, const __grid_constant__ RaggedArgs a, int 
     pdl_trigger();
     int expert = 0, p0 = tt * kT, count = min(kT, a.R - p0);
     if (a.offsets != nullptr) {
-        // position tt is in the group after those that end at or before it
-        int before = 0;
-        for (int e = lane; e < a.E; e += 32) before += a.offsets[e + 1] <= tt;
-        expert = static_cast<int>(__reduce_add_sync(0xffffffffu, before));
+        // position tt is in the group that is the first to end behind it (if offsets descend, as the tiles have it: a
+        // group starts where the ones before it end)
+        int end = a.E;
+        for (int e = a.E - 1 - lane; e >= 0; e -= 32) end = a.offsets[e + 1] > tt ? e : end;
+        expert = static_cast<int>(__reduce_min_sync(0xffffffffu, end));
         if (expert >= a.E || a.offsets[0] > tt) return;
     }
 

@@ -85,3 +85,105 @@ def test_codes_of_tiny_rows(moe):
     rq, rs = quant_ref(x.float().cpu())
     assert torch.equal(s.cpu(), rs)
     assert torch.equal(q.cpu(), rq), "rows %s" % (q.cpu() != rq).any(1).nonzero().flatten().tolist()
+
+
+# ------------------------------------------------------------------ grouped products: wrong and empty groups, odd rows
+
+def clamped(off, R):
+    """Group starts as moe.h has them for wrong offsets: inside 0..R and ascending."""
+    return torch.cummax(off.long().clamp(0, R), 0).values.tolist()
+
+
+def fill_ref(y, x, w, off, ids, k):
+    R, o = y.shape[0], clamped(off, y.shape[0])
+    for e in range(len(o) - 1):
+        lo, hi = o[e], o[e + 1]
+        if lo < hi:
+            rows = (ids[lo:hi].long() % 2 ** 32 // k).clamp(max=x.shape[0] - 1) if ids is not None else slice(lo, hi)
+            y[lo:hi] = (x[rows].to(D) @ w[e].to(D).T).to(F32).to(y.dtype)
+    return y
+
+
+# R, E: by rows (R <= 2/3 E, or 16 rows at most in no more groups), in tiles
+GROUPS = [(12, 64), (12, 12), (300, 900), (40, 8), (700, 8)]
+
+
+@pytest.mark.parametrize("R,E", GROUPS)
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("wrong", ["descending", "negative", "beyond", "late", "random"])
+def test_wrong_offsets_leave_right_groups_right(moe, R, E, gather, wrong):
+    g = gen(R * 3 + E)
+    N, K, k = 36, 200, 2
+    x, w = ints(g, -4, 4, R // k if gather else R, K), ints(g, -4, 4, E, N, K)
+    off = torch.randint(0, R + 1, (E + 1,), generator=g, device="cuda").sort().values
+    off[0], off[E] = 0, R
+    if wrong == "descending":
+        off[1], off[2] = 5, 4
+        off[E // 2:E // 2 + 3] = off[E // 2:E // 2 + 3].flip(0)
+    elif wrong == "negative":
+        off[0], off[1], off[E // 2] = -3, -2 ** 31, -1
+    elif wrong == "beyond":
+        off[E - 1], off[E] = R + 1, 2 ** 31 - 1
+    elif wrong == "late":
+        off[:3] = torch.tensor([4, 2, 5], device="cuda")
+        off[E] = R - 3
+    else:
+        off = torch.randint(-R, 2 * R, (E + 1,), generator=g, device="cuda")
+    off = off.int()
+    ids = torch.randperm(R, generator=g, device="cuda").int() if gather else None
+    if gather:
+        ids[[0, R // 2]] = torch.tensor([-7, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    guard = torch.full((R + 64, N), 5.0, device="cuda", dtype=BF)
+    moe.moe_grouped_gemm(x, w, off, ids, k=k, out=guard[:R])
+    assert (guard[R:] == 5).all()
+    assert torch.equal(guard[:R], fill_ref(torch.full((R, N), 5.0, device="cuda", dtype=BF), x, w, off, ids, k))
+
+
+@pytest.mark.parametrize("R,E", GROUPS)
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_rows_outside_the_groups_stay_either_way(moe, R, E, swiglu):
+    g = gen(R + E)
+    N, K = 20, 136
+    x, w = ints(g, -4, 4, R, K), ints(g, -4, 4, E, 2 * N if swiglu else N, K)
+    off = (5 + (torch.rand(E + 1, generator=g, device="cuda") * (R - 8)).long().sort().values).clamp(max=R - 3).int()
+    for o in (off, torch.zeros_like(off), torch.full_like(off, R)):
+        for dt in (BF, F32):
+            y = torch.full((R, N), 77.0, dtype=dt, device="cuda")
+            moe.moe_grouped_gemm(x, w, o, out=y, out_dtype=dt, swiglu=swiglu)
+            live = torch.zeros(R, dtype=torch.bool, device="cuda")
+            live[int(o[0]):int(o[E])] = True
+            assert (y[~live] == 77).all()
+            if not swiglu:
+                assert torch.equal(y, fill_ref(torch.full_like(y, 77.0), x, w, o, None, 1))
+            else:
+                assert (y[live].abs() <= 49).all()
+
+
+@pytest.mark.parametrize("R,E", GROUPS)
+@pytest.mark.parametrize("K", [8, 200, 520])
+def test_nan_rows_stay_in_their_rows_either_way(moe, R, E, K):
+    g = gen(R + K)
+    N = 33
+    x, w = ints(g, -4, 4, R, K), ints(g, -4, 4, E, N, K)
+    off = torch.randint(0, R + 1, (E + 1,), generator=g, device="cuda").sort().values.int()
+    off[0], off[E] = 0, R
+    ref = moe.moe_grouped_gemm(x, w, off, out_dtype=F32)
+    bad = torch.zeros(R, dtype=torch.bool, device="cuda")
+    bad[[1, R // 2, R - 1]] = True
+    x[bad] = NAN
+    y = moe.moe_grouped_gemm(x, w, off, out_dtype=F32)
+    assert torch.equal(y[~bad], ref[~bad]) and torch.isnan(y[bad]).all()
+
+
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5])
+@pytest.mark.parametrize("N", [1, 2, 3, 5, 127, 1001])
+@pytest.mark.parametrize("K", [16, 272, 4112])
+def test_int8_gemm_of_few_rows_and_odd_columns(moe, M, N, K):
+    g = gen(M * 17 + N + K)
+    q, w = ints(g, -128, 127, M, K, dtype=torch.int8), ints(g, -128, 127, N, K, dtype=torch.int8)
+    qs, ws = torch.rand(M, generator=g, device="cuda") + 0.5, torch.rand(N, generator=g, device="cuda") + 0.5
+    guard = torch.full((M * N + 64,), 5.0, device="cuda")
+    y = moe.moe_int8_gemm(q, qs, w, ws, out=guard[:M * N].view(M, N), out_dtype=F32)
+    ref = int8_ref(q, qs, w, ws)
+    close(y, ref, 4 * 2.0 ** -24 * ref.abs() + 1e-30)
+    assert (guard[M * N:] == 5).all()
