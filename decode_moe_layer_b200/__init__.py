@@ -27,6 +27,7 @@ from ._lib import (  # noqa: F401
     moe_reduce_partials,
     moe_route,
     moe_route_noalloc,
+    moe_selftest_norm_timeout,
     moe_selftest_wait_timeout,
     moe_status_string,
     moe_workspace_bytes,

@@ -24,6 +24,7 @@ EXPORTS = (
     "moe_down_combine", "moe_mxfp4_forward", "moe_workspace_bytes", "moe_forward_launches", "moe_mxfp4_forward_ex",
     "moe_mxfp4_forward_profile", "moe_route_noalloc", "moe_selftest_wait_timeout", "moe_mxfp4_forward_partial",
     "moe_reduce_partials", "moe_block_norm", "moe_int8_quantize", "moe_int8_gemm", "moe_grouped_gemm", "moe_combine",
+    "moe_selftest_norm_timeout",
 )
 PROFILE_KERNELS = ("route_logits", "route_select", "permute", "gate_up", "gather", "gate_up_tc_small",
                    "gate_up_tc_large", "down", "down_tc_small", "down_tc_large", "combine")
@@ -83,6 +84,8 @@ def load():
     F = ctypes.c_float
     lib.moe_block_norm.restype = I
     lib.moe_block_norm.argtypes = [P, P, P, P, I, P, F, F, F, F, P, P, P, P, I, I, P]
+    lib.moe_selftest_norm_timeout.restype = I
+    lib.moe_selftest_norm_timeout.argtypes = [P, P, P, P, P, P, P, P, I, I, P]
     lib.moe_int8_quantize.restype = I
     lib.moe_int8_quantize.argtypes = [P, I, P, P, I, I, P]
     lib.moe_int8_gemm.restype = I
@@ -133,6 +136,14 @@ def moe_selftest_wait_timeout(status_out, stream=None):
     """Launch the bounded-wait self-test: writes MOE_ERR_TIMEOUT into status_out (int32 [1], CUDA)."""
     _need(status_out, torch.int32, "status_out")
     _check(load().moe_selftest_wait_timeout(_ptr(status_out), _stream(stream)), "moe_selftest_wait_timeout")
+
+
+def moe_selftest_norm_timeout(x, residual, w_post, w_pre, res_out, h_out, q_out, q_s, stream=None):
+    """moe_block_norm whose first CTA waits for bytes that never come: its rows become NaN."""
+    M, H = x.shape
+    _check(load().moe_selftest_norm_timeout(_ptr(x), _ptr(residual), _ptr(w_post), _ptr(w_pre), _ptr(res_out),
+                                            _ptr(h_out), _ptr(q_out), _ptr(q_s), M, H, _stream(stream)),
+           "moe_selftest_norm_timeout")
 
 
 def moe_route(x, router_w, k: int, router_bias=None, stream=None):

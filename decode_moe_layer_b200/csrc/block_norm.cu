@@ -283,7 +283,8 @@ __device__ __forceinline__ void bulk_load_once(void *dst, const void *src, uint3
 
 // Many rows: a few CTAs per SM, each with its rows (blockIdx.x, + gridDim.x, ..) on their way through a ring of
 // shared-memory stages (bulk copies of x, residual and a per-element gate), so that loads never wait for a
-// reduction.  What is the same for every row stays in registers in fp32: f_post = block_scale * (w_post + o) *
+// reduction.  A row whose copies have not come within the wait's limit is NaN in every output, and so are the rows
+// behind it: there is no status word, and what the stage held would pass for values.  What is the same for every row stays in registers in fp32: f_post = block_scale * (w_post + o) *
 // channel gate and f_pre = w_pre + o.  With a CTA per row 16384 x 7168 took 340 us; with this ring and
 // packed weights taken apart for every row 175 us and 30 instructions an element, most of the issue slots.
 template <int V, bool kQuant, bool kFullGate>
@@ -307,10 +308,13 @@ block_norm_ring_kernel(const __grid_constant__ NormArgs a, int stages)
     __syncthreads();
     pdl_wait();
     pdl_trigger();
+    const uint32_t lost = blockIdx.x == 0 ? a.waits.lost : 0;
+    int issued = 0;
     auto issue = [&](int s, int row) {   // thread 0
+        ++issued;
         uint8_t *dst = ring + s * inputs * row_bytes;
         const size_t at = static_cast<size_t>(row) * a.H;
-        mbar_arrive_expect_tx(&full[s], inputs * row_bytes);
+        mbar_arrive_expect_tx(&full[s], inputs * row_bytes + lost);
         bulk_load_once(dst, a.x + at, row_bytes, &full[s]);
         if (has_res) bulk_load_once(dst + row_bytes, a.residual + at, row_bytes, &full[s]);
         if (kFullGate) bulk_load_once(dst + gate_at, static_cast<const __nv_bfloat16 *>(a.gate) + at, row_bytes, &full[s]);
@@ -352,8 +356,8 @@ block_norm_ring_kernel(const __grid_constant__ NormArgs a, int stages)
     const f2 rs2 = {a.residual_scale, a.residual_scale};
     int s = 0, parity = 0;
     for (long long row = blockIdx.x; row < a.M; row += gridDim.x) {
-        const float tg = a.gate_kind == MOE_GATE_TOKEN ? static_cast<const float *>(a.gate)[row] : 1.0f;
-        mbar_wait(&full[s], parity, aborted, status);
+        float tg = a.gate_kind == MOE_GATE_TOKEN ? static_cast<const float *>(a.gate)[row] : 1.0f;
+        mbar_wait_for(&full[s], parity, aborted, status, a.waits.limit);
         const uint8_t *st = ring + s * inputs * row_bytes;
         const size_t base = static_cast<size_t>(row) * nvec;
         f2 v[V][4];
@@ -365,6 +369,7 @@ block_norm_ring_kernel(const __grid_constant__ NormArgs a, int stages)
 #pragma unroll
             for (int j = 0; j < 4; ++j) ss = fma2(v[i][j], v[i][j], ss);
         }
+        if (aborted) tg = ss.x = __int_as_float(0x7FFFFFFF);   // by way of the sums the other threads' too
         float scale = tg;
         if (has_post) scale *= rsqrtf(block_sum_max(ss.x + ss.y, 0.f, red[0]).x * inv_h + a.eps);
         const f2 scale2 = {scale, scale};
@@ -415,14 +420,17 @@ block_norm_ring_kernel(const __grid_constant__ NormArgs a, int stages)
                 }
             }
         }
-        __syncthreads();   // the stage has been read, the sums too
+        aborted = __syncthreads_or(aborted);   // the stage has been read, the sums too
         const long long next = row + static_cast<long long>(stages) * gridDim.x;
-        if (threadIdx.x == 0 && next < a.M) issue(s, static_cast<int>(next));
+        if (threadIdx.x == 0 && next < a.M && !aborted) issue(s, static_cast<int>(next));
         if (++s == stages) {
             s = 0;
             parity ^= 1;
         }
     }
+    if (aborted && threadIdx.x == 0)   // copies in flight land while the CTA lives
+        for (int i = max(0, issued - stages); i < issued; ++i)
+            mbar_wait_drain(&full[i % stages], (i / stages) & 1, status, a.waits.limit);
 }
 
 // silu(min(g, 7)) * clamp(u, -7, 7) in fp32, NaN for a NaN.  With t = exp(-|a|), silu(a) = a / (1 + t) or a t / (1 + t): the
@@ -523,13 +531,18 @@ static cudaError_t launch_ring(const NormArgs &a, int threads, cudaStream_t s)
     return full ? launch_ring_t<V, false, true>(a, threads, s) : launch_ring_t<V, false, false>(a, threads, s);
 }
 
-cudaError_t launch_block_norm(const NormArgs &a, cudaStream_t s)
+bool norm_by_ring(int M, int H)
 {
-    const int nvec = a.H / norm::kVec;
     // Without the ring an SM holds several rows at once while a row has at most 512 threads, and one after another
     // beyond.  Both sides (without, with the ring): 7168 columns, 148 rows 3.2 and 3.7 us, 200 rows 5.4 and 4.6, 590
     // rows 10.4 and 6.7; 16384 columns, 200 rows 8.0 and 7.3; 2048 columns, 200 rows 2.3 and 3.5, 590 rows 3.5 and 3.9
-    if (a.M >= norm::kRingRows || (nvec > norm::kWideVecs && a.M > kPlanSMs)) {
+    return M >= norm::kRingRows || (H / norm::kVec > norm::kWideVecs && M > kPlanSMs);
+}
+
+cudaError_t launch_block_norm(const NormArgs &a, cudaStream_t s)
+{
+    const int nvec = a.H / norm::kVec;
+    if (norm_by_ring(a.M, a.H)) {
         // few threads with several vectors each: the reductions cost less, more CTAs hide them (16384 rows of 2048:
         // 50 us with four vectors a thread, 62 with one)
         return nvec <= 64 ? launch_ring<2>(a, row_threads(nvec, 2), s) : launch_ring<4>(a, row_threads(nvec, 4), s);

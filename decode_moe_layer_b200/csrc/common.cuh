@@ -18,9 +18,6 @@ namespace moe {
 
 // ------------------------------------------------------------------ status
 
-// ~2 s at 2 GHz: far above any legitimate wait inside one layer call.
-constexpr long long kWaitLimitCycles = 4000000000LL;
-
 // Where a call's device status goes: the workspace word, and the caller's optional slot.
 struct StatusPtrs {
     int *ws;
@@ -98,29 +95,35 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity)
 
 // Bounded wait for the phase with the given parity to complete.  Once a wait
 // has timed out (`aborted` set) later waits return at once, so every thread
-// still reaches every CTA barrier and the kernel ends.  kLimit is in SM clock
-// cycles (the kernels use kWaitLimitCycles; the wait self-test a short limit).
-template <long long kLimit = kWaitLimitCycles>
-__device__ __forceinline__ void mbar_wait(uint64_t *bar, uint32_t parity, bool &aborted, const StatusPtrs &st)
+// still reaches every CTA barrier and the kernel ends.  The limit is in SM clock
+// cycles (the kernels use kWaitLimitCycles; the self-tests a short limit).
+__device__ __forceinline__ void mbar_wait_for(uint64_t *bar, uint32_t parity, bool &aborted, const StatusPtrs &st,
+                                              long long limit)
 {
     if (aborted) return;
     if (mbar_try_wait(bar, parity)) return;
     long long t0 = clock64();
     while (!mbar_try_wait(bar, parity)) {
-        if (clock64() - t0 > kLimit) {
+        if (clock64() - t0 > limit) {
             aborted = true;
             record_timeout(st);
             return;
         }
     }
 }
+template <long long kLimit = kWaitLimitCycles>
+__device__ __forceinline__ void mbar_wait(uint64_t *bar, uint32_t parity, bool &aborted, const StatusPtrs &st)
+{
+    mbar_wait_for(bar, parity, aborted, st, kLimit);
+}
 
 // Bounded wait for copies already issued to land before a CTA exits.  It runs even after an
 // earlier wait gave up: shared memory must not be released with copies still in flight.
-__device__ __forceinline__ void mbar_wait_drain(uint64_t *bar, uint32_t parity, const StatusPtrs &st)
+__device__ __forceinline__ void mbar_wait_drain(uint64_t *bar, uint32_t parity, const StatusPtrs &st,
+                                                long long limit = kWaitLimitCycles)
 {
     bool gave_up = false;
-    mbar_wait(bar, parity, gave_up, st);
+    mbar_wait_for(bar, parity, gave_up, st, limit);
 }
 
 // ------------------------------------------------------------------ bulk copies (TMA engine)

@@ -12,6 +12,9 @@ namespace moe {
 
 constexpr int kStatusOk = 0;
 constexpr int kStatusTimeout = -5;
+// Limit of a bounded wait, ~2 s at 2 GHz: far above any legitimate wait inside one call; and of the self-tests', ~10 ms.
+constexpr long long kWaitLimitCycles = 4000000000LL;
+constexpr long long kSelfTestWaitCycles = 20000000LL;
 // The call's 256-byte status block: word 0 is the status; words kQueueGateUp and kQueueDown
 // are the grouped kernels' work-queue counters, zeroed by the first kernel of the call.
 constexpr int kQueueGateUp = 8;

@@ -16,6 +16,13 @@ constexpr int kMaxRowElems = 16384;      // longest row of block_norm and of the
 constexpr int kMaxProductDim = 65536;    // N and K of the products
 constexpr int kMaxProductRows = 1 << 22;
 
+// How long a kernel waits for its copies; and, for the self-tests, bytes that its first CTA expects and never gets.
+struct WaitRules {
+    long long limit;
+    uint32_t lost;
+};
+constexpr WaitRules kWaits = {kWaitLimitCycles, 0}, kSelfTestWaits = {kSelfTestWaitCycles, 16};
+
 struct NormArgs {
     const __nv_bfloat16 *x, *residual, *w_post, *w_pre;
     const void *gate;
@@ -25,7 +32,9 @@ struct NormArgs {
     float block_scale, residual_scale, eps, w_offset;
     int gate_kind;
     int M, H;
+    WaitRules waits;
 };
+bool norm_by_ring(int M, int H);   // whether the rows take the kernel that waits for copies
 cudaError_t launch_block_norm(const NormArgs &a, cudaStream_t s);
 cudaError_t launch_int8_quantize(const __nv_bfloat16 *x, bool swiglu, int8_t *q, float *q_s, int M, int K,
                                  cudaStream_t s);

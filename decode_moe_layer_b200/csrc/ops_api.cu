@@ -9,6 +9,12 @@
 #include "ops.h"
 #include "ragged_plan.h"
 
+#define OPS_TRY(expr)                                \
+    do {                                             \
+        cudaError_t _e = (expr);                     \
+        if (_e != cudaSuccess) return cuda_fail(_e); \
+    } while (0)
+
 namespace moe {
 
 static bool is_aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -69,21 +75,10 @@ static int run_ragged(bool int8, bool swiglu, const void *w, uint64_t w_rows, Ra
     return e == cudaSuccess ? MOE_OK : cuda_fail(e);
 }
 
-}  // namespace moe
-
-using namespace moe;
-
-#define OPS_TRY(expr)                                \
-    do {                                             \
-        cudaError_t _e = (expr);                     \
-        if (_e != cudaSuccess) return cuda_fail(_e); \
-    } while (0)
-
-extern "C" {
-
-int moe_block_norm(const void *x, const void *residual, const void *w_post, const void *gate, int gate_kind,
-                   const void *w_pre, float block_scale, float residual_scale, float eps, float w_offset, void *res_out,
-                   void *h_out, int8_t *q_out, float *q_s, int M, int H, cudaStream_t stream)
+static int block_norm(const void *x, const void *residual, const void *w_post, const void *gate, int gate_kind,
+                      const void *w_pre, float block_scale, float residual_scale, float eps, float w_offset,
+                      void *res_out, void *h_out, int8_t *q_out, float *q_s, int M, int H, const WaitRules &waits,
+                      cudaStream_t stream)
 {
     if (M < 0 || H <= 0) return MOE_ERR_INVALID_ARG;
     if (!(eps > 0.0f) || !finite_f(eps) || !finite_f(block_scale) || !finite_f(residual_scale) || !finite_f(w_offset))
@@ -132,8 +127,32 @@ int moe_block_norm(const void *x, const void *residual, const void *w_post, cons
     a.gate_kind = gate_kind;
     a.M = M;
     a.H = H;
+    a.waits = waits;
     OPS_TRY(launch_block_norm(a, stream));
     return MOE_OK;
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int moe_block_norm(const void *x, const void *residual, const void *w_post, const void *gate, int gate_kind,
+                   const void *w_pre, float block_scale, float residual_scale, float eps, float w_offset, void *res_out,
+                   void *h_out, int8_t *q_out, float *q_s, int M, int H, cudaStream_t stream)
+{
+    return block_norm(x, residual, w_post, gate, gate_kind, w_pre, block_scale, residual_scale, eps, w_offset, res_out,
+                      h_out, q_out, q_s, M, H, kWaits, stream);
+}
+
+int moe_selftest_norm_timeout(const void *x, const void *residual, const void *w_post, const void *w_pre, void *res_out,
+                              void *h_out, int8_t *q_out, float *q_s, int M, int H, cudaStream_t stream)
+{
+    if (M <= 0 || H <= 0) return MOE_ERR_INVALID_ARG;
+    if (!norm_by_ring(M, H)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    return block_norm(x, residual, w_post, nullptr, MOE_GATE_NONE, w_pre, 1.0f, 1.0f, 1e-6f, 0.0f, res_out, h_out, q_out,
+                      q_s, M, H, kSelfTestWaits, stream);
 }
 
 int moe_int8_quantize(const void *x_bf16, int swiglu, int8_t *q, float *q_s, int M, int K, cudaStream_t stream)

@@ -10,8 +10,6 @@
 
 namespace moe {
 
-constexpr long long kSelfTestWaitCycles = 20000000LL;   // ~10 ms at 2 GHz
-
 __global__ void wait_timeout_selftest_kernel(int32_t *status_out)
 {
     __shared__ uint64_t bar;

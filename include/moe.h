@@ -298,7 +298,8 @@ int moe_mxfp4_forward_profile(const void *x, const float *router_w, const float 
  * moe_int8_quantize makes them.  h is computed from r' before its rounding.  w_pre is given exactly
  * when h_out or q_out is.  With neither w_post, gate nor residual it is the plain norm before a block.
  * res_out or h_out may be x or residual itself (the same pointer).  H a multiple of 8, at most 16384;
- * eps > 0.  Out of contract: rows whose sum of squares overflows fp32.
+ * eps > 0.  Out of contract: rows whose sum of squares overflows fp32.  A row whose copies into the SM do not
+ * come within the bounded wait is NaN in all its outputs (codes 0).
  */
 int moe_block_norm(const void *x_bf16, const void *residual_bf16, const void *w_post_bf16, const void *gate,
                    int gate_kind, const void *w_pre_bf16, float block_scale, float residual_scale, float eps,
@@ -349,6 +350,16 @@ int moe_grouped_gemm(const void *x_bf16, const void *w_bf16, const int32_t *expe
  */
 int moe_combine(const void *y, int y_f32, const float *topk_w, const int32_t *inv_pos, const void *add_bf16,
                 void *out_bf16, int M, int H, int k, cudaStream_t stream);
+
+/*
+ * Self-test of moe_block_norm's way out when a copy does not come: the operator itself (no gate, factors 1, eps 1e-6)
+ * with waits of about 10 ms, and with a few bytes more expected by the first CTA than are copied.  Rows of that CTA,
+ * row 0 among them, become NaN (codes 0); all others are as ever.  Shapes that copy nothing (fewer than 592 rows, or
+ * with H > 4096 fewer than 149) return MOE_ERR_UNSUPPORTED_SHAPE.
+ */
+int moe_selftest_norm_timeout(const void *x_bf16, const void *residual_bf16, const void *w_post_bf16,
+                              const void *w_pre_bf16, void *res_out_bf16, void *h_out_bf16, int8_t *q_out, float *q_s,
+                              int M, int H, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

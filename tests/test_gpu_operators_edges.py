@@ -187,3 +187,32 @@ def test_int8_gemm_of_few_rows_and_odd_columns(moe, M, N, K):
     ref = int8_ref(q, qs, w, ws)
     close(y, ref, 4 * 2.0 ** -24 * ref.abs() + 1e-30)
     assert (guard[M * N:] == 5).all()
+
+
+# ------------------------------------------------------------------ waits that give up
+
+# 16 and 4 stages' worth of rows a CTA, one row a CTA, rows of one and of several vectors a thread
+@pytest.mark.parametrize("M,H", [(592, 64), (1500, 1024), (700, 8), (20000, 264), (160, 8192), (1000, 16384)])
+@pytest.mark.parametrize("post", [False, True])
+@pytest.mark.parametrize("quantize", [False, True])
+def test_norm_rows_whose_copies_do_not_come_are_nan(moe, M, H, post, quantize):
+    g = gen(M + H)
+    x, r, w = randn(g, M, H), randn(g, M, H), randn(g, H)
+    ref = moe.moe_block_norm(x, residual=r, w_post=w if post else None, w_pre=w, quantize=True)
+    out = [torch.zeros_like(t) for t in ref]
+    moe.moe_selftest_norm_timeout(x, r, w if post else None, w, out[0], out[1], out[2] if quantize else None,
+                                  out[3] if quantize else None)
+    torch.cuda.synchronize()
+    lost = torch.isnan(out[0]).all(1)
+    assert lost[0] and not lost.all()
+    assert torch.isnan(out[1][lost]).all()
+    rows = lost.nonzero().flatten()
+    if rows.numel() > 1:
+        step = int(rows[1])
+        assert step >= 148 and torch.equal(rows, torch.arange(0, M, step, device="cuda"))     # one CTA's
+    assert torch.equal(out[0][~lost], ref[0][~lost]) and torch.equal(out[1][~lost], ref[1][~lost])
+    if quantize:
+        assert torch.isnan(out[3][lost]).all() and (out[2][lost] == 0).all()
+        assert torch.equal(out[2][~lost], ref[2][~lost]) and torch.equal(out[3][~lost], ref[3][~lost])
+    again = moe.moe_block_norm(x, residual=r, w_post=w if post else None, w_pre=w, quantize=True)
+    assert all(torch.equal(a, b) for a, b in zip(again, ref))
