@@ -28,6 +28,7 @@ from ._lib import (  # noqa: F401
     moe_route,
     moe_route_noalloc,
     moe_selftest_norm_timeout,
+    moe_selftest_product_timeout,
     moe_selftest_wait_timeout,
     moe_status_string,
     moe_workspace_bytes,

@@ -24,7 +24,7 @@ EXPORTS = (
     "moe_down_combine", "moe_mxfp4_forward", "moe_workspace_bytes", "moe_forward_launches", "moe_mxfp4_forward_ex",
     "moe_mxfp4_forward_profile", "moe_route_noalloc", "moe_selftest_wait_timeout", "moe_mxfp4_forward_partial",
     "moe_reduce_partials", "moe_block_norm", "moe_int8_quantize", "moe_int8_gemm", "moe_grouped_gemm", "moe_combine",
-    "moe_selftest_norm_timeout",
+    "moe_selftest_norm_timeout", "moe_selftest_product_timeout",
 )
 PROFILE_KERNELS = ("route_logits", "route_select", "permute", "gate_up", "gather", "gate_up_tc_small",
                    "gate_up_tc_large", "down", "down_tc_small", "down_tc_large", "combine")
@@ -86,6 +86,8 @@ def load():
     lib.moe_block_norm.argtypes = [P, P, P, P, I, P, F, F, F, F, P, P, P, P, I, I, P]
     lib.moe_selftest_norm_timeout.restype = I
     lib.moe_selftest_norm_timeout.argtypes = [P, P, P, P, P, P, P, P, I, I, P]
+    lib.moe_selftest_product_timeout.restype = I
+    lib.moe_selftest_product_timeout.argtypes = [I, P, P, P, P, P, P, P, I, I, I, I, I, I, I, P, P]
     lib.moe_int8_quantize.restype = I
     lib.moe_int8_quantize.argtypes = [P, I, P, P, I, I, P]
     lib.moe_int8_gemm.restype = I
@@ -144,6 +146,18 @@ def moe_selftest_norm_timeout(x, residual, w_post, w_pre, res_out, h_out, q_out,
     _check(load().moe_selftest_norm_timeout(_ptr(x), _ptr(residual), _ptr(w_post), _ptr(w_pre), _ptr(res_out),
                                             _ptr(h_out), _ptr(q_out), _ptr(q_s), M, H, _stream(stream)),
            "moe_selftest_norm_timeout")
+
+
+def moe_selftest_product_timeout(x, w, out, status_out, q_s=None, w_s=None, expert_offsets=None, sorted_ids=None,
+                                 k: int = 1, swiglu: bool = False, stream=None):
+    """moe_int8_gemm (x int8) or moe_grouped_gemm whose first CTA waits for bytes that never come: its tiles become NaN
+    and status_out MOE_ERR_TIMEOUT."""
+    int8 = x.dtype == torch.int8
+    _check(load().moe_selftest_product_timeout(int(int8), _ptr(x), _ptr(q_s), _ptr(w), _ptr(w_s), _ptr(expert_offsets),
+                                               _ptr(sorted_ids), _ptr(out), int(out.dtype == torch.float32), int(swiglu),
+                                               out.shape[0] // k, out.shape[1], x.shape[1],
+                                               1 if int8 else w.shape[0], k, _ptr(status_out), _stream(stream)),
+           "moe_selftest_product_timeout")
 
 
 def moe_route(x, router_w, k: int, router_bias=None, stream=None):

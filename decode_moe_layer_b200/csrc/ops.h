@@ -54,6 +54,7 @@ struct RaggedArgs {
     int y_f32;
     int R, M, N, K, E, k;
     int nt, stages, stage_bytes, row_blocks, kblocks, split, ring_bytes, accs, acc_cols;   // ragged_wide.cu
+    WaitRules waits;
 };
 // Maps of the same rows with boxes of 16, 32, .. 128 of them; the first alone, one row high, for the gather.
 struct BoxMaps {

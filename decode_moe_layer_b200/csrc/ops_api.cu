@@ -42,6 +42,7 @@ static int run_ragged(bool int8, bool swiglu, const void *w, uint64_t w_rows, Ra
         return a.status_out ? cudaMemsetAsync(a.status_out, 0, sizeof(int32_t), stream) : cudaSuccess;
     };
     if (ragged_by_rows(a.R, a.E, int8)) {
+        if (a.waits.lost) return MOE_ERR_UNSUPPORTED_SHAPE;   // (the self-test: this kernel waits for nothing)
         cudaError_t e = clear_status();
         if (e == cudaSuccess) e = launch_ragged_rows(int8, swiglu, w, a, stream);
         return e == cudaSuccess ? MOE_OK : cuda_fail(e);
@@ -132,6 +133,88 @@ static int block_norm(const void *x, const void *residual, const void *w_post, c
     return MOE_OK;
 }
 
+static int int8_gemm(const int8_t *q, const float *q_s, const int8_t *w_q, const float *w_s, const void *add_bf16,
+                     void *out, int out_f32, int M, int N, int K, int32_t *status_out, const WaitRules &waits,
+                     cudaStream_t stream)
+{
+    if (M < 0 || N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
+    if (K % 16 != 0 || K > kMaxProductDim || N > kMaxProductDim || M > kMaxProductRows)
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (M == 0) return MOE_OK;
+    if (!q || !q_s || !w_q || !w_s || !out) return MOE_ERR_INVALID_ARG;
+    if (!is_aligned(q, 16) || !is_aligned(w_q, 16) || !is_aligned(out, 16) || !is_aligned(add_bf16, 16) ||
+        !is_aligned(q_s, 4) || !is_aligned(w_s, 4) || !is_aligned(status_out, 4))
+        return MOE_ERR_INVALID_ARG;
+    const size_t mn = static_cast<size_t>(M) * N, on = mn * (out_f32 ? 4 : 2);
+    if (ranges_meet(out, on, q, static_cast<size_t>(M) * K) || ranges_meet(out, on, w_q, static_cast<size_t>(N) * K) ||
+        ranges_meet(out, on, q_s, static_cast<size_t>(M) * 4) || ranges_meet(out, on, w_s, static_cast<size_t>(N) * 4) ||
+        bad_overlap(out, on, add_bf16, mn * 2, out_f32 == 0))
+        return MOE_ERR_INVALID_ARG;
+    if (ranges_meet(status_out, 4, out, on) || ranges_meet(status_out, 4, q, static_cast<size_t>(M) * K) ||
+        ranges_meet(status_out, 4, w_q, static_cast<size_t>(N) * K) ||
+        ranges_meet(status_out, 4, q_s, static_cast<size_t>(M) * 4) ||
+        ranges_meet(status_out, 4, w_s, static_cast<size_t>(N) * 4) || ranges_meet(status_out, 4, add_bf16, mn * 2))
+        return MOE_ERR_INVALID_ARG;
+    RaggedArgs a = {};
+    a.waits = waits;
+    a.x = q;
+    a.K = K;
+    a.row_scale = q_s;
+    a.col_scale = w_s;
+    a.add = static_cast<const __nv_bfloat16 *>(add_bf16);
+    a.y = out;
+    a.y_f32 = out_f32 != 0;
+    a.status_out = status_out;
+    a.R = M;
+    a.M = M;
+    a.N = N;
+    a.E = 1;
+    a.k = 1;
+    return run_ragged(true, false, w_q, static_cast<uint64_t>(N), a, stream);
+}
+
+static int grouped_gemm(const void *x_bf16, const void *w_bf16, const int32_t *expert_offsets,
+                        const int32_t *sorted_ids, void *y, int y_f32, int swiglu, int M, int N, int K, int E, int k,
+                        int32_t *status_out, const WaitRules &waits, cudaStream_t stream)
+{
+    if (M < 0 || N <= 0 || K <= 0 || E <= 0 || k <= 0) return MOE_ERR_INVALID_ARG;
+    if (K % 8 != 0 || K > kMaxProductDim || N > kMaxProductDim || E > kMaxE || k > kMaxK ||
+        static_cast<long long>(M) * k > kMaxProductRows)
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (M == 0) return MOE_OK;
+    if (!x_bf16 || !w_bf16 || !expert_offsets || !y) return MOE_ERR_INVALID_ARG;
+    if (!is_aligned(x_bf16, 16) || !is_aligned(w_bf16, 16) || !is_aligned(y, 16) || !is_aligned(expert_offsets, 4) ||
+        !is_aligned(sorted_ids, 4) || !is_aligned(status_out, 4))
+        return MOE_ERR_INVALID_ARG;
+    const int R = M * k;
+    const int x_rows = sorted_ids ? M : R;
+    const size_t yn = static_cast<size_t>(R) * N * (y_f32 ? 4 : 2);
+    const uint64_t uK = static_cast<uint64_t>(K), uN = static_cast<uint64_t>(N), uE = static_cast<uint64_t>(E);
+    const size_t wn = uE * uN * uK * (swiglu ? 4 : 2);
+    if (ranges_meet(y, yn, x_bf16, static_cast<size_t>(x_rows) * K * 2) || ranges_meet(y, yn, w_bf16, wn) ||
+        ranges_meet(y, yn, expert_offsets, (uE + 1) * 4) || ranges_meet(y, yn, sorted_ids, static_cast<size_t>(R) * 4))
+        return MOE_ERR_INVALID_ARG;
+    if (ranges_meet(status_out, 4, y, yn) || ranges_meet(status_out, 4, x_bf16, static_cast<size_t>(x_rows) * K * 2) ||
+        ranges_meet(status_out, 4, w_bf16, wn) || ranges_meet(status_out, 4, expert_offsets, (uE + 1) * 4) ||
+        ranges_meet(status_out, 4, sorted_ids, static_cast<size_t>(R) * 4))
+        return MOE_ERR_INVALID_ARG;
+    RaggedArgs a = {};
+    a.waits = waits;
+    a.offsets = expert_offsets;
+    a.sorted_ids = sorted_ids;
+    a.x = x_bf16;
+    a.K = K;
+    a.y = y;
+    a.y_f32 = y_f32 != 0;
+    a.status_out = status_out;
+    a.R = R;
+    a.M = x_rows;
+    a.N = N;
+    a.E = E;
+    a.k = k;
+    return run_ragged(false, swiglu != 0, w_bf16, uE * uN * (swiglu ? 2 : 1), a, stream);
+}
+
 }  // namespace moe
 
 using namespace moe;
@@ -172,80 +255,28 @@ int moe_int8_quantize(const void *x_bf16, int swiglu, int8_t *q, float *q_s, int
 int moe_int8_gemm(const int8_t *q, const float *q_s, const int8_t *w_q, const float *w_s, const void *add_bf16,
                   void *out, int out_f32, int M, int N, int K, int32_t *status_out, cudaStream_t stream)
 {
-    if (M < 0 || N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
-    if (K % 16 != 0 || K > kMaxProductDim || N > kMaxProductDim || M > kMaxProductRows)
-        return MOE_ERR_UNSUPPORTED_SHAPE;
-    if (M == 0) return MOE_OK;
-    if (!q || !q_s || !w_q || !w_s || !out) return MOE_ERR_INVALID_ARG;
-    if (!is_aligned(q, 16) || !is_aligned(w_q, 16) || !is_aligned(out, 16) || !is_aligned(add_bf16, 16) ||
-        !is_aligned(q_s, 4) || !is_aligned(w_s, 4) || !is_aligned(status_out, 4))
-        return MOE_ERR_INVALID_ARG;
-    const size_t mn = static_cast<size_t>(M) * N, on = mn * (out_f32 ? 4 : 2);
-    if (ranges_meet(out, on, q, static_cast<size_t>(M) * K) || ranges_meet(out, on, w_q, static_cast<size_t>(N) * K) ||
-        ranges_meet(out, on, q_s, static_cast<size_t>(M) * 4) || ranges_meet(out, on, w_s, static_cast<size_t>(N) * 4) ||
-        bad_overlap(out, on, add_bf16, mn * 2, out_f32 == 0))
-        return MOE_ERR_INVALID_ARG;
-    if (ranges_meet(status_out, 4, out, on) || ranges_meet(status_out, 4, q, static_cast<size_t>(M) * K) ||
-        ranges_meet(status_out, 4, w_q, static_cast<size_t>(N) * K) ||
-        ranges_meet(status_out, 4, q_s, static_cast<size_t>(M) * 4) ||
-        ranges_meet(status_out, 4, w_s, static_cast<size_t>(N) * 4) || ranges_meet(status_out, 4, add_bf16, mn * 2))
-        return MOE_ERR_INVALID_ARG;
-    RaggedArgs a = {};
-    a.x = q;
-    a.K = K;
-    a.row_scale = q_s;
-    a.col_scale = w_s;
-    a.add = static_cast<const __nv_bfloat16 *>(add_bf16);
-    a.y = out;
-    a.y_f32 = out_f32 != 0;
-    a.status_out = status_out;
-    a.R = M;
-    a.M = M;
-    a.N = N;
-    a.E = 1;
-    a.k = 1;
-    return run_ragged(true, false, w_q, static_cast<uint64_t>(N), a, stream);
+    return int8_gemm(q, q_s, w_q, w_s, add_bf16, out, out_f32, M, N, K, status_out, kWaits, stream);
 }
 
 int moe_grouped_gemm(const void *x_bf16, const void *w_bf16, const int32_t *expert_offsets, const int32_t *sorted_ids,
                      void *y, int y_f32, int swiglu, int M, int N, int K, int E, int k, int32_t *status_out,
                      cudaStream_t stream)
 {
-    if (M < 0 || N <= 0 || K <= 0 || E <= 0 || k <= 0) return MOE_ERR_INVALID_ARG;
-    if (K % 8 != 0 || K > kMaxProductDim || N > kMaxProductDim || E > kMaxE || k > kMaxK ||
-        static_cast<long long>(M) * k > kMaxProductRows)
-        return MOE_ERR_UNSUPPORTED_SHAPE;
-    if (M == 0) return MOE_OK;
-    if (!x_bf16 || !w_bf16 || !expert_offsets || !y) return MOE_ERR_INVALID_ARG;
-    if (!is_aligned(x_bf16, 16) || !is_aligned(w_bf16, 16) || !is_aligned(y, 16) || !is_aligned(expert_offsets, 4) ||
-        !is_aligned(sorted_ids, 4) || !is_aligned(status_out, 4))
-        return MOE_ERR_INVALID_ARG;
-    const int R = M * k;
-    const int x_rows = sorted_ids ? M : R;
-    const size_t yn = static_cast<size_t>(R) * N * (y_f32 ? 4 : 2);
-    const uint64_t uK = static_cast<uint64_t>(K), uN = static_cast<uint64_t>(N), uE = static_cast<uint64_t>(E);
-    const size_t wn = uE * uN * uK * (swiglu ? 4 : 2);
-    if (ranges_meet(y, yn, x_bf16, static_cast<size_t>(x_rows) * K * 2) || ranges_meet(y, yn, w_bf16, wn) ||
-        ranges_meet(y, yn, expert_offsets, (uE + 1) * 4) || ranges_meet(y, yn, sorted_ids, static_cast<size_t>(R) * 4))
-        return MOE_ERR_INVALID_ARG;
-    if (ranges_meet(status_out, 4, y, yn) || ranges_meet(status_out, 4, x_bf16, static_cast<size_t>(x_rows) * K * 2) ||
-        ranges_meet(status_out, 4, w_bf16, wn) || ranges_meet(status_out, 4, expert_offsets, (uE + 1) * 4) ||
-        ranges_meet(status_out, 4, sorted_ids, static_cast<size_t>(R) * 4))
-        return MOE_ERR_INVALID_ARG;
-    RaggedArgs a = {};
-    a.offsets = expert_offsets;
-    a.sorted_ids = sorted_ids;
-    a.x = x_bf16;
-    a.K = K;
-    a.y = y;
-    a.y_f32 = y_f32 != 0;
-    a.status_out = status_out;
-    a.R = R;
-    a.M = x_rows;
-    a.N = N;
-    a.E = E;
-    a.k = k;
-    return run_ragged(false, swiglu != 0, w_bf16, uE * uN * (swiglu ? 2 : 1), a, stream);
+    return grouped_gemm(x_bf16, w_bf16, expert_offsets, sorted_ids, y, y_f32, swiglu, M, N, K, E, k, status_out, kWaits,
+                        stream);
+}
+
+int moe_selftest_product_timeout(int int8, const void *x, const float *q_s, const void *w, const float *w_s,
+                                 const int32_t *expert_offsets, const int32_t *sorted_ids, void *y, int y_f32,
+                                 int swiglu, int M, int N, int K, int E, int k, int32_t *status_out,
+                                 cudaStream_t stream)
+{
+    if (M <= 0 || !status_out) return MOE_ERR_INVALID_ARG;
+    if (int8)
+        return int8_gemm(static_cast<const int8_t *>(x), q_s, static_cast<const int8_t *>(w), w_s, nullptr, y, y_f32, M,
+                         N, K, status_out, kSelfTestWaits, stream);
+    return grouped_gemm(x, w, expert_offsets, sorted_ids, y, y_f32, swiglu, M, N, K, E, k, status_out, kSelfTestWaits,
+                        stream);
 }
 
 int moe_combine(const void *y, int y_f32, const float *topk_w, const int32_t *inv_pos, const void *add_bf16,

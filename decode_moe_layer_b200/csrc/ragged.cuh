@@ -214,6 +214,19 @@ __device__ __forceinline__ void store_pair(const RaggedArgs &a, float g, float u
         static_cast<__nv_bfloat16 *>(a.y)[at] = __float2bfloat16_rn(h);
 }
 
+// NaN in column n of `count` rows of y from `row` on.
+__device__ __forceinline__ void store_nan(const RaggedArgs &a, int row, int count, int n)
+{
+    if (n >= a.N) return;
+    const size_t ld = static_cast<size_t>(a.N), at = row * ld + n;
+    for (int j = 0; j < count; ++j) {
+        if (a.y_f32)
+            static_cast<float *>(a.y)[at + j * ld] = __int_as_float(0x7FFFFFFF);
+        else
+            static_cast<__nv_bfloat16 *>(a.y)[at + j * ld] = __ushort_as_bfloat16(0x7FFF);
+    }
+}
+
 // The addend of kCols columns as finish_columns takes it.  The loads are unconditional, the last live column's again
 // past it: behind branches they go out one after the other.
 template <bool kInt8, int kCols>

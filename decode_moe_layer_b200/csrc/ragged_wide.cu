@@ -79,13 +79,14 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t pa
     return ok != 0;
 }
 // mbar_wait for a barrier that the other CTA arrives on too.
-__device__ __forceinline__ void mbar_wait_cluster(uint64_t *bar, uint32_t parity, bool &aborted, const StatusPtrs &st)
+__device__ __forceinline__ void mbar_wait_cluster(uint64_t *bar, uint32_t parity, bool &aborted, const StatusPtrs &st,
+                                                  long long limit)
 {
     if (aborted) return;
     if (mbar_try_wait_cluster(bar, parity)) return;
     const long long t0 = clock64();
     while (!mbar_try_wait_cluster(bar, parity)) {
-        if (clock64() - t0 > kWaitLimitCycles) {
+        if (clock64() - t0 > limit) {
             aborted = true;
             record_timeout(st);
             return;
@@ -107,12 +108,13 @@ __device__ __forceinline__ bool warp_try_wait(uint32_t bar, uint32_t parity)
         : "memory");
     return ok != 0;
 }
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, bool &aborted, const StatusPtrs &st)
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, bool &aborted, const StatusPtrs &st,
+                                          long long limit)
 {
     if (warp_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
     while (!warp_try_wait(bar, parity)) {
-        if (__any_sync(0xffffffffu, clock64() - t0 > kWaitLimitCycles)) {
+        if (__any_sync(0xffffffffu, clock64() - t0 > limit)) {
             aborted = true;
             record_timeout(st);
             return false;
@@ -278,6 +280,7 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         // ------------------------------------------------------------ weights
         Ring ring(a);
         int issued = 0;
+        const uint32_t lost = blockIdx.x == 0 ? a.waits.lost : 0;
         for (; more && !aborted; w.next(), more = w.locate()) {
             const int half = ((w.count + 31) & ~31) >> 1, block = 2 * w.rb + half_id;
             // weight rows past the expert's last come from the next one, or are zeros: nobody stores their products
@@ -285,10 +288,10 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             // of both CTAs, weights and tokens
             const uint32_t bytes = 2 * (kABytes + (kGather ? max(half, 4 * kGatherWarps) : box_rows(a, half, w.halved)) * kStageKBytes);
             for (int kb = kb0; kb < kb1; ++kb, ring.next(), ++issued) {
-                if (!warp_wait(empty0 + ring.bar, ring.parity ^ 1, aborted, status)) break;
+                if (!warp_wait(empty0 + ring.bar, ring.parity ^ 1, aborted, status, a.waits.limit)) break;
                 const uint32_t sa = ring0 + ring.at, bar = full_pair + ring.bar;
                 if (elected) {
-                    if (half_id == 0) expect_tx(full0 + ring.bar, bytes);
+                    if (half_id == 0) expect_tx(full0 + ring.bar, bytes + lost);
                     tma_load_2d_pair(sa, &wmap, kb * kStageK, wrow, bar);   // swiglu: 64 gate rows, then their up rows
                     if (kSwiglu) tma_load_2d_pair(sa + kABytes / 2, &wmap, kb * kStageK, wrow + a.N, bar);
                 }
@@ -298,12 +301,12 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         __syncwarp();
         const int filled = min(issued, a.stages);
         for (int i = issued - filled; i < issued && !aborted; ++i)
-            warp_wait(empty0 + 8 * (i % a.stages), (i / a.stages) & 1, aborted, status);
+            warp_wait(empty0 + 8 * (i % a.stages), (i / a.stages) & 1, aborted, status, a.waits.limit);
         // after a timeout the even CTA waits for both CTAs' copies in flight: the stages before the one it gave up on
         if (aborted && half_id == 0)
             for (int i = 0; i < a.stages && i < issued; ++i) {
                 const int back = issued - 1 - i;
-                mbar_wait_drain(&full[back % a.stages], (back / a.stages) & 1, status);
+                mbar_wait_drain(&full[back % a.stages], (back / a.stages) & 1, status, a.waits.limit);
             }
     } else if (!kGather && warp == 2) {
         // ------------------------------------------------------------ tokens: one box
@@ -311,7 +314,7 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         for (; more && !aborted; w.next(), more = w.locate()) {
             const int half = ((w.count + 31) & ~31) >> 1, map = box_rows(a, half, w.halved) / 16 - 1, row0 = w.p0 + half_id * half;
             for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
-                if (!warp_wait(empty0 + ring.bar, ring.parity ^ 1, aborted, status)) break;
+                if (!warp_wait(empty0 + ring.bar, ring.parity ^ 1, aborted, status, a.waits.limit)) break;
                 if (elected)
                     tma_load_2d_pair(ring0 + ring.at + kABytes, &xmaps.m[map], kb * kStageK, row0, full_pair + ring.bar);
             }
@@ -326,9 +329,9 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             const int b = a.accs > 1 ? i & 1 : 0, n32 = (w.count + 31) & ~31;
             const uint32_t idesc = kInt8 ? umma_idesc_i8(256, n32) : umma_idesc_bf16(256, n32);
             const uint32_t acc = tmem + b * a.acc_cols;
-            if (!warp_wait(smem_u32(&acc_empty[b]), ((i >> 1) & 1) ^ 1, aborted, status)) break;
+            if (!warp_wait(smem_u32(&acc_empty[b]), ((i >> 1) & 1) ^ 1, aborted, status, a.waits.limit)) break;
             for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
-                if (!warp_wait(full0 + ring.bar, ring.parity, aborted, status)) break;
+                if (!warp_wait(full0 + ring.bar, ring.parity, aborted, status, a.waits.limit)) break;
                 tc_fence_after();
                 const uint32_t ad = desc_lo + (ring.at >> 4), bd = ad + (kABytes >> 4);
                 if (elected) {
@@ -345,7 +348,7 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         // the epilogues' last arrivals, of the other CTA too, land while this CTA lives
         if (split == 1)
             for (int j = i > 1 ? i - 2 : 0; j < i; ++j)
-                mbar_wait_cluster(&acc_empty[a.accs > 1 ? j & 1 : 0], (j >> 1) & 1, aborted, status);
+                mbar_wait_cluster(&acc_empty[a.accs > 1 ? j & 1 : 0], (j >> 1) & 1, aborted, status, a.waits.limit);
     } else if (warp >= kEpi0 && warp < kEpi0 + 4 && split == 1) {
         // ------------------------------------------------------------ epilogue
         const int q = warp - kEpi0;
@@ -361,9 +364,10 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 for (int j = threadIdx.x - 32 * kEpi0; j < kNt; j += 128) rs[j] = j < w.count ? a.row_scale[w.p0 + j] : 0.f;
                 asm volatile("bar.sync 1, 128;" ::: "memory");
             }
-            mbar_wait(&acc_full[b], (i >> 1) & 1, aborted, status);
+            mbar_wait_for(&acc_full[b], (i >> 1) & 1, aborted, status, a.waits.limit);
             tc_fence_after();
-            // (after a timeout the rest runs on whatever is there: the warps keep meeting at their barriers)
+            // (after a timeout the rest runs on whatever is there, so that the warps keep meeting at their barriers, and
+            // NaN goes over it at the end)
             const uint32_t acc = tmem + b * a.acc_cols + (static_cast<uint32_t>(32 * q) << 16);
             if (kSwiglu) {
                 // Gate rows are lanes 0..63 (warps q = 0, 1), their up rows lanes 64..127 (q = 2, 3).  Warps q and
@@ -420,7 +424,7 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 idx[i] = static_cast<int>(min(f / static_cast<uint32_t>(a.k), static_cast<uint32_t>(a.M - 1)));
             }
             for (int kb = kb0; kb < kb1; ++kb, ring.next()) {
-                if (!warp_wait(empty0 + ring.bar, ring.parity ^ 1, aborted, status)) break;
+                if (!warp_wait(empty0 + ring.bar, ring.parity ^ 1, aborted, status, a.waits.limit)) break;
                 if (mine)
                     tma_gather4_pair(ring0 + ring.at + kABytes + run * 4 * kStageKBytes, &xmaps.m[0], kb * kStageK, idx,
                                      full_pair + ring.bar);
@@ -454,17 +458,18 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 load_add<kInt8>(a, static_cast<size_t>(t.p0) + c, t.count - c, n, add);
                 asm volatile("bar.sync 1, 256;" ::: "memory");
             }
-            mbar_wait(&acc_full[0], 0, aborted, status);
+            mbar_wait_for(&acc_full[0], 0, aborted, status, a.waits.limit);
             tc_fence_after();
-            if (warp == 0 && lane < split)
+            // (who gave up tells nobody that it is done and sends nothing: its peers' waits give up too)
+            if (warp == 0 && lane < split && !aborted)
                 mbar_arrive_cluster_relaxed(map_cluster(smem_u32(free_all), static_cast<uint32_t>(2 * lane + half_id)));
             if (warp == 1 && lane == 0)
                 mbar_arrive_expect_tx(landed, static_cast<uint32_t>((runs - slice + split - 1) / split * split * kRunBytes));
             __syncwarp();
-            mbar_wait(free_all, 0, aborted, status);
-            __syncwarp();
+            mbar_wait_for(free_all, 0, aborted, status, a.waits.limit);
+            aborted = __any_sync(0xffffffffu, aborted);
             const uint32_t acc = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-            for (int u = group; u < runs; u += 2) {
+            for (int u = group; u < runs && !aborted; u += 2) {
                 uint32_t v[8];
                 tmem_ld8(acc + 8 * u, v);
                 const uint32_t to = static_cast<uint32_t>(2 * (u % split) + half_id), bar = map_cluster(smem_u32(landed), to);
@@ -472,7 +477,7 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 st_async4(at, v, bar);
                 st_async4(at + kRunBytes / 2, v + 4, bar);
             }
-            mbar_wait_cluster(landed, 0, aborted, status);
+            mbar_wait_cluster(landed, 0, aborted, status, a.waits.limit);
             // part of slice s for run i, column half h, accumulator row r
             auto part = [&](int s, int i, int h, int r) {
                 return *reinterpret_cast<const uint4 *>(smem + (s * own + i) * kRunBytes + h * (kRunBytes / 2) + r * 16);
@@ -491,7 +496,7 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 out[2] = p.z;
                 out[3] = p.w;
             };
-            for (int i = group; i * split + slice < runs; i += 2) {
+            for (int i = group; i * split + slice < runs && !aborted; i += 2) {
                 const int c = 8 * (i * split + slice), live = t.count - c;
                 const size_t row0 = static_cast<size_t>(t.p0) + c;
                 if (kSwiglu) {   // two threads per output row, four columns each
@@ -521,6 +526,28 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     if (aborted) {
         cluster_sync();
         __nanosleep(100000);   // parts that others have sent land while this CTA lives
+        // What this warp has stored of the cluster's tiles, or would have, becomes NaN: the sums behind it may lack parts.
+        if (split == 1 ? warp >= kEpi0 && warp < kEpi0 + 4 : warp < 8) {
+            const int q = warp & 3, row = 32 * q + lane;
+            for (TileWalk t(lo, first, a, cluster, clusters); t.locate(); t.next()) {
+                const int block = 2 * t.rb + half_id;
+                if (split == 1 && !kSwiglu) {
+                    store_nan(a, t.p0, t.count, block * kRows + row);
+                } else if (split == 1) {
+                    const int up = 8 * (q >> 1);
+                    for (int c = up; c < t.count; c += 16)
+                        store_nan(a, t.p0 + c, min(8, t.count - c), block * 64 + 32 * (q & 1) + lane);
+                } else {
+                    for (int c = 8 * ((warp >> 2) * split + slice); c < t.count; c += 16 * split) {
+                        const int h = 4 * (row >> 6);
+                        if (kSwiglu)
+                            store_nan(a, t.p0 + c + h, min(4, t.count - c - h), block * 64 + (row & 63));
+                        else
+                            store_nan(a, t.p0 + c, min(8, t.count - c), block * kRows + row);
+                    }
+                }
+            }
+        }
     } else {
         cluster_sync_relaxed();
     }

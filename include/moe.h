@@ -320,7 +320,8 @@ int moe_int8_quantize(const void *x_bf16, int swiglu, int8_t *q, float *q_s, int
  * q int8 [M,K], q_s fp32 [M]; w_q int8 [N,K], w_s fp32 [N]; add bf16 [M,N] (nullable); out bf16 [M,N],
  * or fp32 when out_f32.  The sum is exact (int32).  A bf16 out may be add itself.  Any M and N up to
  * 4194304 and 65536; K a multiple of 16, at most 65536.  status_out (nullable, device int32) receives
- * MOE_OK or MOE_ERR_TIMEOUT once the enqueued work has run.
+ * MOE_OK or MOE_ERR_TIMEOUT once the enqueued work has run; elements that a wait which gave up left without
+ * their sum are NaN, with or without status_out.
  */
 int moe_int8_gemm(const int8_t *q, const float *q_s, const int8_t *w_q, const float *w_s, const void *add_bf16,
                   void *out, int out_f32, int M, int N, int K, int32_t *status_out, cudaStream_t stream);
@@ -335,7 +336,7 @@ int moe_int8_gemm(const int8_t *q, const float *q_s, const int8_t *w_q, const fl
  * sorted_ids is NULL.  expert_offsets int32 [E+1] and sorted_ids int32 [M*k] as moe_permute writes them;
  * offsets ascend within 0..M*k.  Positions outside every range are left as they were in y.
  * y bf16 [M*k,N], or fp32 when y_f32.  bf16 products, fp32 sums.  K a multiple of 8 up to 65536, N up to
- * 65536, E <= 1024, k <= 32, M*k <= 4194304.  status_out as in moe_int8_gemm.
+ * 65536, E <= 1024, k <= 32, M*k <= 4194304.  status_out and timeouts as in moe_int8_gemm.
  */
 int moe_grouped_gemm(const void *x_bf16, const void *w_bf16, const int32_t *expert_offsets, const int32_t *sorted_ids,
                      void *y, int y_f32, int swiglu, int M, int N, int K, int E, int k, int32_t *status_out,
@@ -360,6 +361,17 @@ int moe_combine(const void *y, int y_f32, const float *topk_w, const int32_t *in
 int moe_selftest_norm_timeout(const void *x_bf16, const void *residual_bf16, const void *w_post_bf16,
                               const void *w_pre_bf16, void *res_out_bf16, void *h_out_bf16, int8_t *q_out, float *q_s,
                               int M, int H, cudaStream_t stream);
+
+/*
+ * The same for the products in tiles: moe_int8_gemm (int8 != 0; no addend) or moe_grouped_gemm with waits of about 10
+ * ms, and with a few bytes more expected by the first CTA than are copied.  status_out (not NULL) receives
+ * MOE_ERR_TIMEOUT; what the tiles of that CTA's cluster give becomes NaN, all else is as ever.  Shapes that are not
+ * computed in tiles return MOE_ERR_UNSUPPORTED_SHAPE.
+ */
+int moe_selftest_product_timeout(int int8, const void *x, const float *q_s, const void *w, const float *w_s,
+                                 const int32_t *expert_offsets, const int32_t *sorted_ids, void *y, int y_f32,
+                                 int swiglu, int M, int N, int K, int E, int k, int32_t *status_out,
+                                 cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -216,3 +216,56 @@ def test_norm_rows_whose_copies_do_not_come_are_nan(moe, M, H, post, quantize):
         assert torch.equal(out[2][~lost], ref[2][~lost]) and torch.equal(out[3][~lost], ref[3][~lost])
     again = moe.moe_block_norm(x, residual=r, w_post=w if post else None, w_pre=w, quantize=True)
     assert all(torch.equal(a, b) for a, b in zip(again, ref))
+
+
+def lost_and_right(y, ref, status):
+    """Mask of the NaN of y, once all else is what it should be."""
+    assert status.item() == -5
+    lost = torch.isnan(y)
+    assert torch.equal(y[~lost], ref[~lost]) and lost.any() and not lost.all()
+    return lost
+
+
+# one tile a cluster, with K cut among two and four pairs and not; several tiles a cluster, the last in halves
+@pytest.mark.parametrize("M,N,K,once", [(33, 1536, 2048, True), (128, 1536, 2048, True), (40, 1000, 8192, True), (6, 700, 4096, True),
+                                        (256, 4096, 7168, True), (64, 520, 144, True), (200, 1024, 768, True),
+                                        (2500, 4096, 400, False), (1500, 4100, 2000, False)])
+@pytest.mark.parametrize("out_dtype", [BF, F32])
+def test_int8_tiles_whose_copies_do_not_come_are_nan(moe, M, N, K, once, out_dtype):
+    g = gen(M + N + K)
+    q, w = ints(g, -128, 127, M, K, dtype=torch.int8), ints(g, -128, 127, N, K, dtype=torch.int8)
+    qs, ws = torch.rand(M, generator=g, device="cuda") + 0.5, torch.rand(N, generator=g, device="cuda") + 0.5
+    ref = moe.moe_int8_gemm(q, qs, w, ws, out_dtype=out_dtype)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = torch.full_like(ref, 3.0)
+    moe.moe_selftest_product_timeout(q, w, y, status, q_s=qs, w_s=ws)
+    lost = lost_and_right(y, ref, status)
+    assert lost[0, :256].all()
+    if once:      # a tile of 256 columns, whole
+        assert (lost[:, :256] == lost[:, :1]).all() and not lost[:, 256:].any()
+    z = moe.moe_int8_gemm(q, qs, w, ws, out_dtype=out_dtype, status_out=status)
+    assert status.item() == 0 and torch.equal(z, ref)
+
+
+@pytest.mark.parametrize("cuts,N,K", [([3, 20, 20, 60], 768, 2048), ([0, 40, 48, 100], 600, 4096), ([2, 300, 700, 701, 1200], 4096, 136),
+                                      ([0, 90], 1024, 4096), ([0, 129, 258, 387, 516, 3000], 1024, 136)])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_grouped_tiles_whose_copies_do_not_come_are_nan(moe, cuts, N, K, gather, swiglu):
+    R, E = cuts[-1] + 5, len(cuts) - 1
+    g = gen(R + N)
+    x, w = randn(g, R, K), randn(g, E, 2 * N if swiglu else N, K, scale=K ** -0.5)
+    off = torch.tensor(cuts, dtype=torch.int32, device="cuda")
+    ids = torch.randperm(R, generator=g, device="cuda").int() if gather else None
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for dt in (BF, F32):
+        ref = moe.moe_grouped_gemm(x, w, off, ids, swiglu=swiglu, out=torch.full((R, N), 7.0, dtype=dt, device="cuda"),
+                                   out_dtype=dt)
+        y = torch.full((R, N), 7.0, dtype=dt, device="cuda")
+        moe.moe_selftest_product_timeout(x, w, y, status, expert_offsets=off, sorted_ids=ids, swiglu=swiglu)
+        lost = lost_and_right(y, ref, status)
+        first = 128 if swiglu else 256
+        assert lost[cuts[0], :first].all()
+        assert (lost[:, :first] == lost[:, :1]).all()
+        z = moe.moe_grouped_gemm(x, w, off, ids, swiglu=swiglu, out=y.fill_(7), out_dtype=dt, status_out=status)
+        assert status.item() == 0 and torch.equal(z, ref)
