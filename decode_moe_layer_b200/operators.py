@@ -14,10 +14,25 @@ import torch
 from ._lib import MoEError, load
 
 load()
-from . import _ops  # noqa: E402  (resolves its symbols in libmoe.so)
 
 
-_ops.raise_as(MoEError)
+class _Unbuilt:
+    """In the place of _ops where it is missing or does not load: the layer needs only libmoe.so, and so does importing the
+    package; the functions below raise."""
+
+    def __init__(self, cause):
+        self._cause = cause
+
+    def __getattr__(self, name):
+        raise ImportError("_ops.so not built, or not for this torch: run `python decode_moe_layer_b200/build.py`") \
+            from self._cause
+
+
+try:
+    from . import _ops  # (resolves its symbols in libmoe.so)
+    _ops.raise_as(MoEError)
+except ImportError as e:
+    _ops = _Unbuilt(e)
 
 
 def _on(stream, fn, *args):

@@ -1,5 +1,11 @@
 """How the operators around the layer refuse and fail, as far as it needs no GPU."""
 import ctypes
+import os
+import shutil
+import subprocess
+import sys
+
+import pytest
 
 import decode_moe_layer_b200 as moe
 
@@ -29,3 +35,34 @@ def test_product_selftest_refusals():
         assert call(int8, st=0x4000000) == INV and call(int8, K=1020) == UNS
         assert call(int8, M=4, E=64) == UNS            # by rows: nothing is waited for
     assert call(0, off=0) == INV and call(0, M=64, E=96) == UNS
+
+
+@pytest.mark.parametrize("binding", ["missing", "broken"])
+def test_without_the_binding_the_layer_imports_and_the_operators_say_what_to_do(tmp_path, binding):
+    here = os.path.dirname(moe.LIB_PATH)
+    pkg = tmp_path / "decode_moe_layer_b200"
+    pkg.mkdir()
+    for f in os.listdir(here):
+        if f.endswith(".py"):
+            shutil.copy(os.path.join(here, f), str(pkg))
+    os.symlink(moe.LIB_PATH, str(pkg / "libmoe.so"))
+    if binding == "broken":
+        (pkg / "_ops.so").write_bytes(b"no library")
+    code = """
+import torch, decode_moe_layer_b200 as moe
+assert moe.__file__.startswith(%r)
+assert moe.moe_workspace_bytes(2, 1024, 512, 16, 4) > 0 and callable(moe.moe_mxfp4_forward)
+x = torch.zeros(2, 32)
+for call in (lambda: moe.moe_block_norm(x), lambda: moe.moe_int8_quantize(x), lambda: moe.moe_int8_gemm(x, x, x, x),
+             lambda: moe.moe_grouped_gemm(x, x, x), lambda: moe.moe_combine(x, x, x)):
+    try:
+        call()
+    except ImportError as e:
+        assert "build.py" in str(e) and e.__cause__ is not None, e
+    else:
+        raise AssertionError("no error")
+print("ok")
+""" % str(tmp_path)
+    r = subprocess.run([sys.executable, "-c", code], cwd=str(tmp_path), capture_output=True, text=True, timeout=300,
+                       env=dict(os.environ, PYTHONPATH=str(tmp_path)))
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
