@@ -22,6 +22,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe.so")
 BINDING_SRC = os.path.join(CSRC, "python_ops.cpp")
 BINDING = os.path.join(HERE, "_ops.so")
+BINDING_KEY = os.path.join(ROOT, "_build", "_ops.key")
 CUDA_HOME = os.environ.get("CUDA_HOME", "/usr/local/cuda")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
@@ -54,21 +55,33 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 
 def build_binding(force: bool = False) -> str:
-    deps = [BINDING_SRC, os.path.join(ROOT, "include", "moe.h")]
-    if not force and os.path.exists(BINDING) and all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps):
-        return BINDING
+    """_ops.so is made for one torch and one Python: besides its sources' times it is kept by a key of the command and of
+    their versions, written beside the objects."""
     import torch
     base = os.path.dirname(torch.__file__)
+    command = [
+        "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-Wall",
+        "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch.compiled_with_cxx11_abi()),
+        "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(base, "include"),
+        "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+        "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(CUDA_HOME, "include"),
+        BINDING_SRC, "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
+        "-ltorch_cuda", "-lc10", "-lc10_cuda", "-L", HERE, "-lmoe", "-Wl,-rpath,$ORIGIN"]
+    key = "\n".join([torch.__version__, str(sysconfig.get_config_var("SOABI"))] + command)
+    deps = [BINDING_SRC, os.path.join(ROOT, "include", "moe.h")]
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps):
+        try:
+            with open(BINDING_KEY) as f:
+                if f.read() == key:
+                    return BINDING
+        except OSError:
+            pass
     tmp = BINDING + ".tmp%d" % os.getpid()
-    subprocess.check_call(
-        ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-Wall",
-         "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch.compiled_with_cxx11_abi()),
-         "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(base, "include"),
-         "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
-         "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(CUDA_HOME, "include"),
-         BINDING_SRC, "-o", tmp, "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
-         "-ltorch_cuda", "-lc10", "-lc10_cuda", "-L", HERE, "-lmoe", "-Wl,-rpath,$ORIGIN"])
+    subprocess.check_call(command + ["-o", tmp])
     os.replace(tmp, BINDING)
+    os.makedirs(os.path.dirname(BINDING_KEY), exist_ok=True)
+    with open(BINDING_KEY, "w") as f:
+        f.write(key)
     return BINDING
 
 

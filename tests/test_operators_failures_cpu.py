@@ -1,11 +1,13 @@
 """How the operators around the layer refuse and fail, as far as it needs no GPU."""
 import ctypes
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
 
 import pytest
+import torch
 
 import decode_moe_layer_b200 as moe
 
@@ -66,3 +68,43 @@ print("ok")
     r = subprocess.run([sys.executable, "-c", code], cwd=str(tmp_path), capture_output=True, text=True, timeout=300,
                        env=dict(os.environ, PYTHONPATH=str(tmp_path)))
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
+
+
+def test_binding_is_rebuilt_for_another_torch_or_command(tmp_path, monkeypatch):
+    path = os.path.join(os.path.dirname(moe.LIB_PATH), "build.py")
+    spec = importlib.util.spec_from_file_location("_binding_build", path)
+    b = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(b)
+    calls = []
+
+    def compile_(command):
+        calls.append(command)
+        with open(command[command.index("-o") + 1], "w") as f:
+            f.write("binding")
+
+    src = tmp_path / "python_ops.cpp"
+    src.write_text("source")
+    monkeypatch.setattr(b.subprocess, "check_call", compile_)
+    monkeypatch.setattr(b, "BINDING", str(tmp_path / "_ops.so"))
+    monkeypatch.setattr(b, "BINDING_KEY", str(tmp_path / "objects" / "_ops.key"), raising=False)
+    monkeypatch.setattr(b, "BINDING_SRC", str(src))
+    for _ in range(2):
+        assert b.build_binding() == b.BINDING
+    assert len(calls) == 1                                    # kept
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "0.0.1")
+        b.build_binding()
+        b.build_binding()
+    assert len(calls) == 2                                    # another torch
+    b.build_binding()
+    assert len(calls) == 3
+    with monkeypatch.context() as m:
+        m.setattr(torch, "compiled_with_cxx11_abi", lambda: not torch._C._GLIBCXX_USE_CXX11_ABI)
+        b.build_binding()
+    assert len(calls) == 4                                    # another ABI
+    b.build_binding()
+    os.utime(str(src), (4e9, 4e9))
+    b.build_binding()
+    assert len(calls) == 6                                    # a newer source
+    b.build_binding(force=True)
+    assert len(calls) == 7
