@@ -396,7 +396,7 @@ ragged_wide_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                     __nv_bfloat16 add[kEpiCols];
                     load_add<kInt8>(a, row, w.count - c, n, add);
                     uint32_t v[kEpiCols];
-                    tmem_ld(acc + c, v);
+                    tmem_ld16(acc + c, v);
                     finish_columns<kInt8, kEpiCols>(a, v, rs + c, cs, add, row, w.count - c, n);
                 }
             }
