@@ -269,3 +269,18 @@ def test_grouped_tiles_whose_copies_do_not_come_are_nan(moe, cuts, N, K, gather,
         assert (lost[:, :first] == lost[:, :1]).all()
         z = moe.moe_grouped_gemm(x, w, off, ids, swiglu=swiglu, out=y.fill_(7), out_dtype=dt, status_out=status)
         assert status.item() == 0 and torch.equal(z, ref)
+
+
+# ------------------------------------------------------------------ in place
+
+@pytest.mark.parametrize("M,H", [(700, 1024), (160, 8192), (3000, 264)])     # rows through the ring of copies
+@pytest.mark.parametrize("gate", [False, True])
+def test_norm_in_place_of_many_rows(moe, M, H, gate):
+    g = gen(M + 1)
+    x, r, w = randn(g, M, H), randn(g, M, H), randn(g, H)
+    kw = dict(w_post=w, w_pre=w, gate=randn(g, M, H) if gate else None, quantize=True)
+    ref = moe.moe_block_norm(x, residual=r, **kw)
+    for swap in (False, True):
+        a, b = x.clone(), r.clone()
+        got = moe.moe_block_norm(a, residual=b, res_out=a if swap else b, h_out=b if swap else a, **kw)
+        assert got[0] is (a if swap else b) and all(torch.equal(u, v) for u, v in zip(got, ref))
