@@ -57,23 +57,26 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8])
 // comparing 254 v with (2 n + 1) max, whose products an FMA completes to all their bits: the rounded s would decide ties
 // at random, and ties are common (bf16 rows hold max / 2, whose code is 63.5).  Rounded with a division each, the codes
 // took 2.5 times as long as their memory traffic.  Rows whose scale is below 2^-100, where 1 / s may overflow and the
-// products' last bits fall below fp32's smallest number, are decided one by one after a multiplication by 2^100; their
-// scale, as it is stored, may be denormal or 0.
+// products' last bits fall below fp32's smallest number, are decided one by one after a multiplication by 2^100 (their
+// inv has a minus sign); their scale, as it is stored, may be denormal or 0.
 struct CodeScale {
-    float s, inv, top;
+    float s, inv, top;   // inv 0: a row of zeros, with NaN or with Inf
     __device__ __forceinline__ explicit CodeScale(float max_abs) : s(max_abs / 127.0f), inv(0.f), top(max_abs)
     {
-        if (s > 0x1p-100f) inv = 1.0f / s;
+        if (s > 0x1p-100f)
+            inv = 1.0f / s;
+        else if (top > 0.f)
+            inv = -127.0f / (top * 0x1p100f);
     }
 };
 // One such code (not inlined: 32 copies of it cost the quantiser a quarter of its speed).
 __device__ __noinline__ uint32_t int8_code_exact(float v, float inv, float max_abs)
 {
-    if (inv == 0.f) {
-        if (!(max_abs > 0.f && max_abs < 1.f)) return 0;   // zeros, NaN or Inf
+    if (inv == 0.f) return 0;
+    if (inv < 0.f) {
         v *= 0x1p100f;
         max_abs *= 0x1p100f;
-        inv = 127.f / max_abs;
+        inv = -inv;
     }
     const float t = v * inv, r = rintf(t), n2 = 2.f * r + (t >= r ? 1.f : -1.f);   // n2 / 2: the half next to t
     const float a = 254.f * 0x1p-8f, top = max_abs * 0x1p-8f;   // (no overflow for the largest rows)
@@ -93,11 +96,11 @@ __device__ __forceinline__ uint2 int8_codes8(const float (&f)[8], const CodeScal
         c[i] = __float_as_uint(m);
         far = fmaxf(far, fabsf(t - (m - kMagic)));
     }
-    if (!(far < 0.4999f) || k.inv == 0.f) {
+    if (!(far < 0.4999f) || !(k.inv > 0.f)) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float t = f[i] * k.inv;
-            if (!(fabsf(t - rintf(t)) < 0.4999f) || k.inv == 0.f) c[i] = int8_code_exact(f[i], k.inv, k.top);
+            if (!(fabsf(t - rintf(t)) < 0.4999f) || !(k.inv > 0.f)) c[i] = int8_code_exact(f[i], k.inv, k.top);
         }
     }
     return make_uint2(prmt(prmt(c[0], c[1], 0x0040u), prmt(c[2], c[3], 0x0040u), 0x5410u),
