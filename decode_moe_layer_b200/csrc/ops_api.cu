@@ -1,5 +1,5 @@
 // ops_api.cu -- C entry points of the operators around the routed layer (declared in include/moe.h):
-// argument checks and TMA maps.  None of them needs a workspace, waits for the device or allocates.
+// argument checks and TMA maps, and the self-tests that run them with waits that give up.  None of them needs a workspace, waits for the device or allocates.
 #include <cstring>
 
 #include <cuda.h>

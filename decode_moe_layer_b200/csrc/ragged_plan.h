@@ -9,11 +9,18 @@ namespace moe {
 // ------------------------------------------------------------------ by weight rows or by tiles
 
 // Measured on this part (times on the GPU, weights out of L2), by rows against tiles:
-//  * int8, codes and product: 4096 x 7168 with 4 tokens 11.9 us against 11.5, 1536 x 2048 5.7 against 6.9, 7168 x 2048
-//    7.6 against 8.9; with 8 tokens the rows take about twice their time with 4, the tiles no longer.
+//  * int8, codes and product: 4 tokens 4096 x 7168 11.7 us against 11.8, 16384 x 7168 25.3 against 24.4, 1536 x 2048 5.3
+//    against 7.0, 7168 x 2048 7.2 against 9.1, so within 4% for large weights and ahead for small ones; with 8 tokens the
+//    rows take about twice their time with 4, the tiles no longer.
 //  * grouped, 128 experts of 1536 x 2048, top-8: 4, 8, 12 tokens 28, 52, 69 us against 35, 53, 67; 256 experts of 7168 x
 //    2048: 8, 16, 20, 32 tokens 235, 414, 495, 727 us against 237, 416, 505, 681.  From about 0.7 rows a group on, groups
 //    of two and more rows pay for a tile.
+//    That is of routing that spreads.  The host knows only R and E: by rows an expert's weights are read once a row, in
+//    tiles once, so where few experts get the rows this rule is wrong, by up to seven times: 128 experts of 1536 x 2048, 40
+//    rows over 35, 15, 1 of them 35, 25, 21 us against 36, 23, 10, 80 rows over 63, 22, 1 of them 64, 44, 40 against 62, 28,
+//    11; 256 of 2048 x 2048, 160 rows over 116, 35, 1 of them 141, 108, 106 against 143, 52, 15; 1024 of 512 x 1024, 680 rows
+//    over 502, 96, 1 of them 80, 63, 61 against 103, 49, 25, and 80 rows over 78, 23, 1 of them 15, 12, 11 against 47, 39, 24
+//    (a CTA goes through all the groups to find its tile's).
 //  * with 16 rows at most the call is so short that the tiles' set-up decides: 4 tokens x 4 of 16 experts of 1024 x 1024
 //    7.1 us against 8.4, 1 token 3.7 against 7.4.
 constexpr int kRowsMaxTokens = 4;    // int8
@@ -23,7 +30,6 @@ inline bool ragged_by_rows(int R, int E, bool int8)
     if (int8) return R <= kRowsMaxTokens;
     return 3LL * R <= 2LL * E || (R <= kRowsMaxShort && R <= E);
 }
-
 
 // ------------------------------------------------------------------ tiles (ragged_wide.cu)
 

@@ -5,8 +5,9 @@ Argument marshalling only, most of it compiled (csrc/python_ops.cpp, built as _o
 tensors of a call are on one CUDA device, which need not be the current one; the work is enqueued on that
 device's current stream, or on `stream`, in which case outputs are allocated for that stream and inputs are
 recorded on it.  Two new outputs of a call that take up to 1 MB together share one allocation (each is contiguous
-and starts on a multiple of 512 bytes).  Tensors of another type, shape, layout or device raise ValueError (TypeError if they are no
-tensors), what the C ABI refuses raises MoEError."""
+and starts on a multiple of 512 bytes).  Tensors of another type, shape, layout or device raise ValueError (TypeError if
+they are no tensors), what the C ABI refuses raises MoEError.  Inference only, like the layer: outputs have no autograd
+history, whatever the inputs require."""
 from __future__ import annotations
 
 import torch
