@@ -115,8 +115,8 @@ __device__ __forceinline__ float max_or_nan(float a, float b)
     return r;
 }
 
-// Sum and maximum (NaN if there is one) of a pair over the CTA; every thread gets both.  `buf` holds one pair per warp and is
-// free again after the next call's barrier on the other buffer (callers alternate two).
+// Sum and maximum (NaN if there is one) of a pair over the CTA; every thread gets both.  `buf` holds one pair per
+// warp and is free again after the next call's barrier on the other buffer (callers alternate two).
 __device__ __forceinline__ float2 block_sum_max(float sum, float mx, float2 *buf)
 {
 #pragma unroll
